@@ -1,9 +1,10 @@
-"""Build libspecverify.so in-tree with hipcc for gfx950.
+"""Build libspecverify.so and libspecverify_ops.so in-tree with hipcc for gfx950.
 
 Usage: ``python -m speculative_decoding_sampling_amd.build`` (or
 ``__graft_entry__.build()``).  Compiles every source under ``csrc/`` to an
-object in ``_build/`` in parallel and links the shared library next to this
-file, where the Python binding loads it.
+object in ``_build/`` in parallel and links the two shared libraries next to
+this file, where the Python bindings load them.  libspecverify_ops calls
+libspecverify's public entry points and finds it in its own folder.
 """
 
 import os
@@ -18,11 +19,13 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecverify.so")
+OPS_LIB = os.path.join(HERE, "libspecverify_ops.so")
 
 ARCH = "gfx950"
 SOURCES = ["specverify.hip", "row_stats.hip", "accept.hip", "sample.hip", "filter.hip",
            "filter_rows.hip", "sample_list.hip", "diagnostics.hip", "round_policy.hip",
            "lm_head.hip", "small.hip"]
+OPS_SOURCES = ["ops.hip", "probs.hip", "hidden_norm.hip", "fp8_head.hip"]
 # Packed FP32 instructions stay off: the compiler must not form v_pk_* FP32 ops.
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
@@ -47,20 +50,28 @@ def _run(cmd):
     return out
 
 
+def _object(src):
+    return os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+
+
+def _link(hipcc, lib, sources, *extra):
+    tmp = lib + ".tmp"
+    out = _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp,
+                *map(_object, sources), *extra])
+    os.replace(tmp, lib)
+    return out
+
+
 def build(verbose=False):
     hipcc = _hipcc()
     os.makedirs(BUILD, exist_ok=True)
-    objs = []
-    cmds = []
-    for src in SOURCES:
-        obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        objs.append(obj)
-        cmds.append([hipcc, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
+    cmds = [[hipcc, *FLAGS, "-c", os.path.join(CSRC, src), "-o", _object(src)]
+            for src in SOURCES + OPS_SOURCES]
     with ThreadPoolExecutor(max_workers=min(len(cmds), os.cpu_count() or 1, 8)) as ex:
         outs = list(ex.map(_run, cmds))
-    tmp = LIB + ".tmp"
-    outs.append(_run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]))
-    os.replace(tmp, LIB)
+    outs.append(_link(hipcc, LIB, SOURCES))
+    outs.append(_link(hipcc, OPS_LIB, OPS_SOURCES, "-L", HERE, "-lspecverify",
+                      "-Wl,-rpath,$ORIGIN"))
     if verbose:
         for o in outs:
             if o.strip():

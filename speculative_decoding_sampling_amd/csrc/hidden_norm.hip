@@ -1,0 +1,233 @@
+// The norms around the target's last block, its gate and its residual scale
+// in one pass (specv_hidden_norm):
+//
+//   r' = r + scale * g * N(x; w1),  y = N(r'; w2),  N(v; w) = w v / sqrt(mean(v^2) + eps)
+//
+// Every row is read once, kept in registers through both reductions and
+// written once (r' and y), so the bytes moved are the floor; a workgroup owns
+// a row, each thread 8 values at a time (16-byte loads of bfloat16), as many
+// threads as the row has such groups, up to 1024.  The sums of squares are
+// float32: per thread in order, then the wave on DPP moves, then the waves
+// through LDS in a fixed order.
+//
+// y is formed from r' before r' is rounded to its own type: one rounding less
+// between the residual stream and the logits.
+#include "fp8.h"
+#include "specverify_ops.h"
+
+namespace specv {
+
+constexpr int kNormMaxThreads = 1024;
+
+struct NormArgs {
+  const void* x;
+  const void* r;
+  const void* w1;       // null: x as it is
+  const void* gate;     // null: a factor of one
+  const void* w2;
+  void* r_out;
+  void* out;
+  uint8_t* out_scale;
+  int D, rows_per_gate;
+  bool w_bf16;          // type of w1, gate and w2
+  float scale, eps;
+};
+
+// Values e0 .. e0 + 7 of a row as floats; those at or past D read as 0.
+template <typename T, bool VEC>
+__device__ __forceinline__ void norm_load(const T* row, int e0, int D, float* v) {
+  if constexpr (VEC) {
+    if (e0 < D) {                                        // D is a multiple of 8
+#pragma unroll
+      for (int i = 0; i < 8; i += Elem<T>::kPerVec) load_vec_fast(row, e0 + i, v + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = e0 + i < D ? to_f32(row[e0 + i]) : 0.f;
+  }
+}
+
+// The same for a weight row of either type (uniform over the grid).
+template <bool VEC>
+__device__ __forceinline__ void norm_load_w(const void* w, bool w_bf16, size_t off, int e0, int D,
+                                            float* v) {
+  if (w_bf16) norm_load<bf16_t, VEC>(static_cast<const bf16_t*>(w) + off, e0, D, v);
+  else norm_load<float, VEC>(static_cast<const float*>(w) + off, e0, D, v);
+}
+
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(bf16_t* p, float v) { *p = (bf16_t)bf16_bits(v); }
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void norm_store(T* row, int e0, int D, const float* v) {
+  if constexpr (VEC) {
+    if (e0 >= D) return;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(row + e0) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(row + e0 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint4 w;
+      w.x = bf16_bits(v[0]) | bf16_bits(v[1]) << 16;
+      w.y = bf16_bits(v[2]) | bf16_bits(v[3]) << 16;
+      w.z = bf16_bits(v[4]) | bf16_bits(v[5]) << 16;
+      w.w = bf16_bits(v[6]) | bf16_bits(v[7]) << 16;
+      *reinterpret_cast<uint4*>(row + e0) = w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e0 + i < D) put(row + e0 + i, v[i]);
+  }
+}
+
+// Sum over the workgroup, the same value in every thread.  Two calls use two
+// arrays, so the second needs no barrier before it.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = wave_sum(v);
+  const int nw = blockDim.x / kWave;
+  if (nw == 1) return v;
+  if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int i = 0; i < nw; ++i) s += red[i];
+  return s;
+}
+
+// Rows of more than 2 groups per thread leave the residual in memory until
+// the first reduction is done: with both rows in registers 1024 threads
+// would spill.
+template <typename X, typename R, int OUT, int NV, bool VEC>
+__global__ __launch_bounds__(kNormMaxThreads) void hidden_norm_kernel(NormArgs a) {
+  constexpr bool kEarly = NV <= 2;
+  __shared__ float red[2][kNormMaxThreads / kWave];
+  const int m = blockIdx.x, D = a.D;
+  const size_t off = (size_t)m * D;
+  const X* x = static_cast<const X*>(a.x) + off;
+  const R* r = static_cast<const R*>(a.r) + off;
+  const size_t goff = (size_t)(m / a.rows_per_gate) * D;
+
+  float h[NV][8], res[kEarly ? NV : 1][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e0 = (threadIdx.x + j * blockDim.x) * 8;
+    norm_load<X, VEC>(x, e0, D, h[j]);
+    if constexpr (kEarly) norm_load<R, VEC>(r, e0, D, res[j]);
+  }
+  float f = a.scale;
+  if (a.w1) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
+    f = a.scale / sqrtf(block_sum(ss, red[0]) / (float)D + a.eps);
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e0 = (threadIdx.x + j * blockDim.x) * 8;
+    float c[8];
+    if (a.w1) {
+      norm_load_w<VEC>(a.w1, a.w_bf16, 0, e0, D, c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] *= c[i];
+    }
+    if (a.gate) {
+      norm_load_w<VEC>(a.gate, a.w_bf16, goff, e0, D, c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] *= c[i];
+    }
+    float* rj = res[kEarly ? j : 0];
+    if constexpr (!kEarly) norm_load<R, VEC>(r, e0, D, rj);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      h[j][i] = fmaf(f, h[j][i], rj[i]);
+      ss = fmaf(h[j][i], h[j][i], ss);
+    }
+    norm_store<R, VEC>(static_cast<R*>(a.r_out) + off, e0, D, h[j]);
+  }
+  f = 1.f / sqrtf(block_sum(ss, red[1]) / (float)D + a.eps);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e0 = (threadIdx.x + j * blockDim.x) * 8;
+    float c[8];
+    norm_load_w<VEC>(a.w2, a.w_bf16, 0, e0, D, c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] *= h[j][i] * f;
+    if constexpr (OUT == SPECV_OUT_E4M3) {
+      // 16 lanes hold a run of 128; D is a multiple of it, so a run is wholly
+      // inside the row or wholly past it
+      uint32_t byte;
+      const uint2 q = fp8_pack8(c, byte);
+      if (e0 < D) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + off + e0) = q;
+        if (threadIdx.x % kFp8Lanes == 0) a.out_scale[(off + e0) / kFp8Block] = (uint8_t)byte;
+      }
+    } else if constexpr (OUT == SPECV_OUT_F32) {
+      norm_store<float, VEC>(static_cast<float*>(a.out) + off, e0, D, c);
+    } else {
+      norm_store<bf16_t, VEC>(static_cast<bf16_t*>(a.out) + off, e0, D, c);
+    }
+  }
+}
+
+template <typename X, typename R, int OUT, int NV>
+void norm_launch(const NormArgs& a, int M, int threads, bool vec, hipStream_t stream) {
+  if (vec) hidden_norm_kernel<X, R, OUT, NV, true><<<dim3(M), dim3(threads), 0, stream>>>(a);
+  else hidden_norm_kernel<X, R, OUT, NV, false><<<dim3(M), dim3(threads), 0, stream>>>(a);
+}
+
+template <typename X, typename R, int OUT>
+void norm_by_size(const NormArgs& a, int M, bool vec, hipStream_t stream) {
+  const int groups = (a.D + 7) / 8;
+  const int threads = groups >= kNormMaxThreads ? kNormMaxThreads
+                                                : (groups + kWave - 1) / kWave * kWave;
+  const int nv = (groups + threads - 1) / threads;
+  if (nv == 1) norm_launch<X, R, OUT, 1>(a, M, threads, vec, stream);
+  else if (nv == 2) norm_launch<X, R, OUT, 2>(a, M, threads, vec, stream);
+  else norm_launch<X, R, OUT, 8>(a, M, threads, vec, stream);
+}
+static_assert(SPECV_MAX_D <= 8 * 8 * kNormMaxThreads, "a row fits a workgroup's registers");
+
+template <typename X, typename R>
+void norm_by_out(const NormArgs& a, int M, int out, bool vec, hipStream_t stream) {
+  if (out == SPECV_OUT_E4M3) norm_by_size<X, R, SPECV_OUT_E4M3>(a, M, vec, stream);
+  else if (out == SPECV_OUT_BF16) norm_by_size<X, R, SPECV_OUT_BF16>(a, M, vec, stream);
+  else norm_by_size<X, R, SPECV_OUT_F32>(a, M, vec, stream);
+}
+
+hipError_t launch_hidden_norm(const void* x, bool xb, const void* r, bool rb, const void* w1,
+                              const void* gate, int gate_rows, const void* w2, bool wb, int M,
+                              int D, float scale, float eps, void* r_out, void* out, int out_dtype,
+                              uint8_t* out_scale, hipStream_t stream) {
+  NormArgs a;
+  a.x = x;
+  a.r = r;
+  a.w1 = w1;
+  a.gate = gate;
+  a.w2 = w2;
+  a.r_out = r_out;
+  a.out = out;
+  a.out_scale = out_scale;
+  a.D = D;
+  a.rows_per_gate = gate ? M / gate_rows : 1;
+  a.w_bf16 = wb;
+  a.scale = scale;
+  a.eps = eps;
+  auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  const bool vec = D % 8 == 0 && al(x) && al(r) && al(w1) && al(gate) && al(w2) && al(r_out) &&
+                   (out_dtype == SPECV_OUT_E4M3 || al(out));
+  if (xb) {
+    if (rb) norm_by_out<bf16_t, bf16_t>(a, M, out_dtype, vec, stream);
+    else norm_by_out<bf16_t, float>(a, M, out_dtype, vec, stream);
+  } else {
+    if (rb) norm_by_out<float, bf16_t>(a, M, out_dtype, vec, stream);
+    else norm_by_out<float, float>(a, M, out_dtype, vec, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace specv

@@ -1,0 +1,304 @@
+"""The LM head on 8-bit floats on the GPU against the fp64 reference.
+
+Quantising is exact arithmetic but for the one rounding to e4m3: bytes must be
+equal.  With small integers and scales in a narrow range every float32 sum of
+the product is exact, so the logits must be equal too (bfloat16: the exact sum
+rounded to nearest even).  On general inputs the float32 accumulation of D
+products is off by at most D roundings, each at most 2 u of the sum of
+magnitudes should the matrix core truncate (u = 2^-24): 2 D u sum |h w|, plus
+half a step of the output type.
+"""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import oracle as O  # noqa: E402
+import speculative_decoding_sampling_amd as S  # noqa: E402
+from oracle import operators as OP  # noqa: E402
+from speculative_decoding_sampling_amd import binding  # noqa: E402
+from tests.parity import compare, to_numpy  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32, E4, E8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def bytes_of(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def dev(q, s):
+    return (torch.from_numpy(q).to(DEV).view(E4), torch.from_numpy(s).to(DEV).view(E8))
+
+
+def integers(R, D, top, lo, hi, seed):
+    """Small integers as e4m3 bytes and scales 2^lo .. 2^hi."""
+    rng = np.random.default_rng(seed)
+    q = OP.to_e4m3(rng.integers(-top, top + 1, (R, D)).astype(np.float64))
+    q[q == 0x80] = 0
+    return q, rng.integers(127 + lo, 128 + hi, (R, D // 128)).astype(np.uint8)
+
+
+@pytest.mark.parametrize("R,D,dtype", [(1, 128, F32), (3, 384, BF), (5, 4096, F32), (257, 256, BF),
+                                       (2, 65536, BF)])
+def test_quantize_bytes_are_exact(R, D, dtype):
+    rng = np.random.default_rng(R + D)
+    x = rng.normal(size=(R, D)) * np.exp(3 * rng.normal(size=(R, 1))) * \
+        np.exp(rng.normal(size=(R, D)))
+    x[0, :128] = 0
+    x = torch.from_numpy(x).to(dtype)
+    q, s = S.quantize_fp8(x.to(DEV))
+    wq, ws = OP.quantize(x.double().numpy())
+    assert np.array_equal(bytes_of(s), ws) and np.array_equal(bytes_of(q), wq)
+
+
+def test_quantize_every_float_near_the_grid():
+    # every e4m3 value, the midpoints between neighbours and their neighbours
+    v = OP.e4m3_values()[:0x7f]
+    mid = (v[1:] + v[:-1]) / 2
+    x = np.concatenate([v, mid, np.nextafter(mid.astype(np.float32), np.float32(0)),
+                        np.nextafter(mid.astype(np.float32), np.float32(1e9))]).astype(np.float32)
+    x = np.concatenate([x, -x])
+    rows = []
+    for i in range(0, len(x), 127):
+        row = np.zeros(128, np.float32)
+        part = x[i:i + 127]
+        row[:len(part)] = part
+        row[127] = 448.0                                # the scale is one
+        rows.append(row)
+    x = np.stack(rows)
+    for f in (1.0, 2.0 ** 20, 2.0 ** -100):
+        q, s = S.quantize_fp8(torch.from_numpy(x * np.float32(f)).to(DEV))
+        wq, ws = OP.quantize((x * np.float32(f)).astype(np.float64))
+        assert np.array_equal(bytes_of(s), ws) and np.array_equal(bytes_of(q), wq), f
+
+
+def test_quantize_borders_of_the_scale_and_extremes():
+    top = [448.0, np.nextafter(np.float32(448), np.float32(500)), 224.0, 3.4e38, 1e-38, 1e-45, 2.0 ** -118,
+           2.0 ** -126, np.inf, np.nan, -np.inf, -448.5]
+    x = np.zeros((len(top), 256), np.float32)
+    for i, t in enumerate(top):
+        x[i, 3], x[i, 130] = t, 1.0
+    q, s = S.quantize_fp8(torch.from_numpy(x).to(DEV))
+    wq, ws = OP.quantize(x.astype(np.float64))
+    assert np.array_equal(bytes_of(s), ws), (bytes_of(s)[:, 0], ws[:, 0])
+    assert np.array_equal(bytes_of(q), wq)
+
+
+SIZES = [
+    # M, V, D: row tiles (1 .. past several blocks), vocabulary tails, odd runs
+    (1, 1, 128), (1, 32, 256), (2, 33, 384), (5, 1000, 640), (6, 4097, 4096), (16, 300, 1152),
+    (31, 257, 512), (32, 256, 512), (33, 255, 512), (64, 511, 1024), (65, 513, 896), (96, 1000, 128),
+    (100, 2000, 1152), (127, 640, 512), (128, 640, 640), (129, 640, 768), (160, 999, 2048),
+    (161, 777, 384), (320, 1025, 1024), (321, 640, 256), (577, 1300, 512), (1100, 520, 384),
+]
+
+
+@pytest.mark.parametrize("M,V,D", SIZES)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_exact_on_integers(M, V, D, dtype):
+    print(f"[fp8] M={M} V={V} D={D} {dtype}", flush=True)
+    hq, hs = integers(M, D, 8, 0, 2, 1)
+    wq, ws = integers(V, D, 4, -2, 0, 2)
+    packed = S.pack_fp8_lm_head(*dev(wq, ws))
+    got = S.fp8_lm_head(*dev(hq, hs), packed, dtype=dtype)
+    want = OP.dequantize(hq, hs) @ OP.dequantize(wq, ws).T
+    assert np.abs(want).max() < 2.0 ** 22
+    assert torch.equal(got.cpu(), torch.from_numpy(want).to(dtype)), \
+        int((got.cpu() != torch.from_numpy(want).to(dtype)).sum())
+
+
+@pytest.mark.parametrize("M,V,D", [(5, 2000, 4096), (40, 700, 1152), (130, 900, 2048), (330, 600, 4096),
+                                   (3, 64, 65536), (70, 300, 16384)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_general_inputs_within_the_accumulation_bound(M, V, D, dtype):
+    print(f"[fp8] general M={M} V={V} D={D} {dtype}", flush=True)
+    rng = np.random.default_rng(M)
+    hq, hs = OP.quantize(rng.normal(size=(M, D)) * np.exp(rng.normal(size=(1, D))))
+    wq, ws = OP.quantize(rng.normal(size=(V, D)) * np.exp(rng.normal(size=(V, 1))) / np.sqrt(D))
+    h, w = OP.dequantize(hq, hs), OP.dequantize(wq, ws)
+    got = S.fp8_lm_head(*dev(hq, hs), S.pack_fp8_lm_head(*dev(wq, ws)), dtype=dtype)
+    want = h @ w.T
+    tol = 2 * D * 2.0 ** -24 * (np.abs(h) @ np.abs(w).T)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(err <= tol + torch.finfo(dtype).eps / 2 * (np.abs(want) + tol))
+    # the bound is loose; what is computed is far nearer
+    print("  max error / bound %.2e" % float(np.max(err / (tol + torch.finfo(dtype).eps / 2 * np.abs(want)))))
+
+
+def test_scales_of_every_size():
+    # wide scales: products stay exact, one run per row and column carries all
+    M, V, D = 40, 96, 1152
+    hq, hs = integers(M, D, 8, 0, 0, 3)
+    wq, ws = integers(V, D, 4, 0, 0, 4)
+    nb = D // 128
+    for m in range(M):
+        hq[m].reshape(nb, 128)[np.arange(nb) != m % nb] = 0
+        hs[m] = 127 + (m - 20) * 2
+    ws[:] = 127 + (np.arange(V) % 41 - 20)[:, None]
+    want = OP.dequantize(hq, hs) @ OP.dequantize(wq, ws).T
+    for rep in (1, 5):                                  # both row-tile families
+        got = S.fp8_lm_head(*dev(np.tile(hq, (rep, 1)), np.tile(hs, (rep, 1))),
+                            S.pack_fp8_lm_head(*dev(wq, ws)), dtype=F32)
+        assert np.array_equal(got.cpu().numpy(), np.tile(want, (rep, 1)).astype(np.float32))
+
+
+@pytest.mark.parametrize("M", [7, 200])
+def test_nan_stays_in_its_row_and_column(M):
+    V, D = 300, 512
+    hq, hs = integers(M, D, 8, 0, 2, 5)
+    wq, ws = integers(V, D, 4, -2, 0, 6)
+    want = S.fp8_lm_head(*dev(hq, hs), S.pack_fp8_lm_head(*dev(wq, ws)), dtype=F32).cpu()
+    hq[2, 77], hs[4, 1], wq[9, 500], ws[299, 3] = 0x7f, 255, 0xff, 255
+    got = S.fp8_lm_head(*dev(hq, hs), S.pack_fp8_lm_head(*dev(wq, ws)), dtype=F32).cpu()
+    rows = [m for m in range(M) if m not in (2, 4)]
+    cols = [v for v in range(V) if v not in (9, 299)]
+    assert got[2].isnan().all() and got[4].isnan().all()
+    assert got[:, 9].isnan().all() and got[:, 299].isnan().all()
+    assert torch.equal(got[rows][:, cols], want[rows][:, cols])
+
+
+def test_pack_from_values_and_layout():
+    rng = np.random.default_rng(8)
+    V, D = 70, 640
+    w = torch.from_numpy(rng.normal(size=(V, D))).to(BF).to(DEV)
+    q, s = S.quantize_fp8(w)
+    a, b = S.pack_fp8_lm_head(w), S.pack_fp8_lm_head(q, s)
+    assert torch.equal(a.data, b.data) and (a.V, a.D) == (V, D)
+    p, qn, sn = a.data.cpu().numpy(), bytes_of(q), bytes_of(s)
+    pieces = p[:96 * D].reshape(3, 5, 4, 64, 16)
+    for g, kb, st, l in ((0, 0, 0, 0), (1, 3, 2, 40), (2, 4, 3, 5), (2, 0, 1, 6)):
+        v, k = 32 * g + l % 32, 128 * kb + 64 * (l // 32) + 16 * st
+        assert np.array_equal(pieces[g, kb, st, l], qn[v, k:k + 16] if v < V else np.zeros(16))
+    words = p[96 * D:].reshape(3, 2, 32, 4)
+    assert words[1, 1, 2, 0] == sn[34, 4] and words[1, 1, 2, 1] == 127
+    assert words[2, 0, 3, 2] == sn[67, 2] and (words[2, :, 6:] == 127).all()
+
+
+@pytest.mark.parametrize("M,V", [(6, 3000), (200, 3000), (6, 3001), (200, 3001)])
+def test_rows_around_the_logits_are_left(M, V):
+    D = 256
+    h, w = dev(*integers(M, D, 8, 0, 2, 9)), dev(*integers(V, D, 4, -2, 0, 10))
+    for dtype in (BF, F32):
+        big = torch.full((M + 2, V), 77.0, dtype=dtype, device=DEV)
+        packed = S.pack_fp8_lm_head(*w)
+        S.fp8_lm_head(*h, packed, dtype=dtype, logits=big[1:M + 1])
+        assert (big[0] == 77).all() and (big[M + 1] == 77).all()
+        assert torch.equal(big[1:M + 1], S.fp8_lm_head(*h, packed, dtype=dtype))
+
+
+def test_logits_past_32_bits():
+    # more than 2^31 logits: the rows at the end are those of a small call
+    M, V, D = 560, 4000003, 128
+    rng = np.random.default_rng(11)
+    h = dev(*integers(M, D, 8, 0, 2, 12))
+    w = torch.from_numpy(rng.integers(-4, 5, (4099, D))).to(DEV).to(F32)
+    big = w.repeat((V + 4098) // 4099, 1)[:V].contiguous()
+    out = S.fp8_lm_head(*h, S.pack_fp8_lm_head(big))
+    del big
+    ref = S.fp8_lm_head(*h, S.pack_fp8_lm_head(w))
+    for m in (0, 300, M - 1):
+        for v0 in (0, 4099 * 500, 4099 * 975):
+            n = min(4099, V - v0)
+            assert torch.equal(out[m, v0:v0 + n], ref[m, :n])
+
+
+def test_streams_graphs_and_repeats():
+    for M in (6, 150):
+        a, b = dev(*integers(M, 640, 8, 0, 2, 13)), dev(*integers(M, 640, 8, 0, 2, 14))
+        packed = S.pack_fp8_lm_head(*dev(*integers(2000, 640, 4, -2, 0, 15)))
+        ra, rb = S.fp8_lm_head(*a, packed), S.fp8_lm_head(*b, packed)
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            x, y = S.fp8_lm_head(*a, packed, stream=s1), S.fp8_lm_head(*b, packed, stream=s2)
+            torch.cuda.synchronize()
+            assert torch.equal(x, ra) and torch.equal(y, rb)
+        st = [t.clone() for t in a]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = S.fp8_lm_head(*st, packed)
+        for src, want in ((b, rb), (a, ra), (b, rb)):
+            for t, v in zip(st, src):
+                t.view(torch.uint8).copy_(v.view(torch.uint8))
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(res, want)
+            assert torch.equal(S.fp8_lm_head(*a, packed), ra)
+
+
+def draft_inputs(B, K, V, seed, ragged=True):
+    g = torch.Generator().manual_seed(seed)
+    dl = (torch.randn(B, K, V, generator=g) * 3).to(BF)
+    tok = torch.randint(0, V, (B, K), generator=g, dtype=torch.int32)
+    if K:
+        e = torch.empty(B, K, V).exponential_(generator=g)
+        tok = (torch.softmax(dl.float(), -1) / e).argmax(-1).int()
+    n = torch.randint(0, K + 1, (B,), generator=g, dtype=torch.int32) if ragged else \
+        torch.full((B,), K, dtype=torch.int32)
+    return dict(draft_logits=dl, draft_tokens=tok, draft_len=n, u=torch.rand(B, K, generator=g),
+                u_final=torch.rand(B, generator=g))
+
+
+@pytest.mark.parametrize("B,K,V,D,T,top_k,top_p,eos", [
+    (1, 0, 500, 128, 1.0, 0, 1.0, -1),
+    (4, 3, 5000, 256, 1.0, 0, 1.0, -1),
+    (8, 4, 20000, 512, 0.8, 50, 0.9, 3),
+    (40, 4, 6001, 640, 1.3, 0, 0.9, -1),
+    (70, 4, 9000, 384, 1.0, 0, 1.0, 5),
+])
+def test_verification_on_the_logits(B, K, V, D, T, top_k, top_p, eos):
+    print(f"[fp8] verify B={B} K={K} V={V} D={D} T={T} top_k={top_k} top_p={top_p}", flush=True)
+    rng = np.random.default_rng(B + V)
+    w = torch.from_numpy(rng.normal(size=(V, D)) * 2 / np.sqrt(D)).to(BF).to(DEV)
+    h = torch.from_numpy(rng.normal(size=(B, K + 1, D))).to(BF).to(DEV)
+    packed = S.pack_fp8_lm_head(w)
+    q, s = S.quantize_fp8(h)
+    d = draft_inputs(B, K, V, B)
+    # drafts that the target often accepts: its own logits with noise
+    logits = S.fp8_lm_head(q, s, packed)
+    d["draft_logits"] = (logits[:, :K].float().cpu() + 0.5 * torch.randn(B, K, V, generator=torch.Generator().manual_seed(1))).to(BF)
+    tp = float(np.float32(top_p))
+    for b in range(B):
+        for k in range(K):
+            P, _ = O.processed_distribution(d["draft_logits"][b, k].double().numpy(), T, top_k, tp)
+            d["draft_tokens"][b, k] = O.icdf(P, float(rng.random()))[0]
+    g = {k: v.to(DEV) for k, v in d.items()}
+    res = S.verify_fp8_lm_head(q, s, packed, **g, temperature=T, eos_id=eos, top_k=top_k, top_p=top_p,
+                               debug=True)
+    torch.cuda.synchronize()
+    assert torch.equal(res["target_logits"], logits)
+    bits = res["target_logits"].view(torch.int16).cpu().numpy().view(np.uint16)
+    dbits = d["draft_logits"].view(torch.int16).numpy().view(np.uint16)
+    ora = O.verify(bits, dbits, d["draft_tokens"].numpy(), d["draft_len"].numpy(), d["u"].numpy(),
+                   d["u_final"].numpy(), T, top_k, tp, eos, "bf16")
+    rep = compare(to_numpy({k: v for k, v in res.items() if k != "target_logits"}), ora, K)
+    assert not rep["mismatches"], rep["mismatches"][:4]
+
+
+def test_python_refusals():
+    h, w = dev(*integers(4, 256, 8, 0, 2, 1)), dev(*integers(50, 256, 4, 0, 0, 2))
+    packed = S.pack_fp8_lm_head(*w)
+    with pytest.raises(ValueError):
+        S.quantize_fp8(torch.zeros(4, 200, device=DEV))
+    with pytest.raises(TypeError):
+        S.quantize_fp8(torch.zeros(4, 256, device=DEV, dtype=torch.float16))
+    with pytest.raises(TypeError):
+        S.fp8_lm_head(h[0].view(torch.uint8), h[1], packed)
+    with pytest.raises(ValueError):
+        S.fp8_lm_head(h[0], h[1][:, :1], packed)
+    with pytest.raises(ValueError):
+        S.fp8_lm_head(h[0][:, :128].contiguous(), h[1][:, :1].contiguous(), packed)
+    with pytest.raises(TypeError):
+        S.fp8_lm_head(*h, w[0])
+    with pytest.raises(TypeError):
+        S.fp8_lm_head(*h, packed, dtype=torch.float16)
+    with pytest.raises(S.SpecVerifyError):
+        S.fp8_lm_head(h[0][:0], h[1][:0], packed)
+    with pytest.raises(S.SpecVerifyError) as e:
+        d = {k: v.to(DEV) for k, v in draft_inputs(2, 1, 50, 3).items()}
+        S.verify_fp8_lm_head(h[0].view(2, 2, 256), h[1].view(2, 2, 2), packed, **d,
+                             workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    assert e.value.status == binding.SPECV_EWORKSPACE
