@@ -104,7 +104,8 @@ SPECV_OPS_API specv_status_t specv_fp8_quantize(const void *x, specv_dtype_t dty
  * Pack it once, when the model is loaded.
  *
  * The packed weight is [ceil(V/32)][D/128][4][64] 16-byte pieces: piece
- * (g, kb, s, l) holds q[32 g + l % 32][128 kb + 64 (l / 32) + 16 s .. + 15],
+ * (g, kb, s, l) holds q[32 g + l % 32][128 kb + 64 (s / 2) + 32 (l / 32) +
+ * 16 (s % 2) .. + 15],
  * zeros past V; then [ceil(V/32)][ceil(D/512)][32] 4-byte words of scale
  * bytes: byte i of word (g, j, r) is scale[32 g + r][4 j + i], 127 past the
  * end.

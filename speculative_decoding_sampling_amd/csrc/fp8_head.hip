@@ -13,11 +13,11 @@
 // result holds one hidden row, col l % 32, and vocabulary rows 8 (i / 4) +
 // i % 4 + 4 (l / 32) of accumulator register i.
 //
-// k order.  Per run of 128 lane l supplies bytes 64 (l / 32) .. + 63 of its
-// row, 32 for each of the two products of the run; both operands share that
-// order, and any order of k shared by both gives the same sum.  Both products
-// lie in one run, so a lane's scale byte is that of its row and run whatever
-// the matrix core's own 32-wide blocks are.
+// k order.  A run of 128 is two products of 64; in product j lane l supplies
+// bytes 64 j + 32 (l / 32) .. + 31 of its row.  Both operands share that order,
+// and any order of k shared by both gives the same sum.  Both products lie in
+// one run, so a lane's scale byte is that of its row and run whatever the
+// matrix core's own 32-wide blocks are.
 #include "fp8.h"
 #include "specverify_ops.h"
 
@@ -25,6 +25,8 @@ namespace specv {
 
 typedef int fp8_i32x8 __attribute__((ext_vector_type(8)));
 typedef float fp8_f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 fp8_bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 fp8_bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kF8Group = 32;                       // vocabulary rows of a packed group
 constexpr int kF8RunBytes = kF8Group * kFp8Block;  // packed bytes of one group's run (4 KB)
@@ -94,7 +96,7 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const uint8_t* __restrict
     r /= 4;
     const int kb = (int)(r % nkb);
     const size_t v = r / nkb * kF8Group + lane % 32;
-    const int k = kb * kFp8Block + 64 * (lane / 32) + 16 * s;
+    const int k = kb * kFp8Block + 64 * (s / 2) + 32 * (lane / 32) + 16 * (s % 2);
     uint4 val = make_uint4(0u, 0u, 0u, 0u);
     if (v < (size_t)V) val = *reinterpret_cast<const uint4*>(q + v * D + k);
     *reinterpret_cast<uint4*>(packed + i * 16) = val;
@@ -126,21 +128,91 @@ hipError_t launch_fp8_pack(const uint8_t* q, const uint8_t* scale, void* packed,
 
 // -------------------------------------------------------------- product
 
-__device__ __forceinline__ fp8_i32x8 fp8_operand(uint4 lo, uint4 hi) {
-  fp8_i32x8 r = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,
-                 (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-  return r;
+// 32 bytes of a lane's row, one operand of a 64-wide product step.
+struct Fp8Bytes {
+  uint4 lo, hi;
+};
+
+// c += a b over one 64-wide step of run I of its group (byte I of the scale
+// words).
+//
+// The 8-bit matrix product keeps, of each 8 products it adds at once, what
+// lies within 2^-13 of the largest (measured on single products): the logits
+// come out 1e-5 to 6e-5 of their size off, a hundredth of a bfloat16 step and
+// less.  That is enough where they are rounded to bfloat16.  Float32 logits
+// (EXACT) take the bfloat16 product instead, on operands that hold the same
+// values exactly with their scales applied: 5e-9 to 3e-8 off, at half the
+// rate.
+template <bool EXACT, int I>
+__device__ __forceinline__ fp8_f32x16 fp8_step(const Fp8Bytes& a, const Fp8Bytes& b, fp8_f32x16 c,
+                                               uint32_t sa, uint32_t sb) {
+  const uint32_t aw[8] = {a.lo.x, a.lo.y, a.lo.z, a.lo.w, a.hi.x, a.hi.y, a.hi.z, a.hi.w};
+  const uint32_t bw[8] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w, b.hi.x, b.hi.y, b.hi.z, b.hi.w};
+  if constexpr (!EXACT) {
+    fp8_i32x8 av, bv;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      av[i] = (int)aw[i];
+      bv[i] = (int)bw[i];
+    }
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 0, 0, I, (int)sa, I, (int)sb);
+  } else {
+    const float fa = __uint_as_float(((sa >> (8 * I)) & 255u) << 23);
+    const float fb = __uint_as_float(((sb >> (8 * I)) & 255u) << 23);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      fp8_bf16x8 x, y;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const fp8_bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(aw[2 * s + w], fa, false);
+        const fp8_bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(aw[2 * s + w], fa, true);
+        const fp8_bf16x2 y0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bw[2 * s + w], fb, false);
+        const fp8_bf16x2 y1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bw[2 * s + w], fb, true);
+        x[4 * w] = x0[0];
+        x[4 * w + 1] = x0[1];
+        x[4 * w + 2] = x1[0];
+        x[4 * w + 3] = x1[1];
+        y[4 * w] = y0[0];
+        y[4 * w + 1] = y0[1];
+        y[4 * w + 2] = y1[0];
+        y[4 * w + 3] = y1[1];
+      }
+      c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
+    }
+    return c;
+  }
 }
 
-// One product step of run i (0..3, its byte of the scale words).
-template <int I>
-__device__ __forceinline__ fp8_f32x16 fp8_mfma(fp8_i32x8 a, fp8_i32x8 b, fp8_f32x16 c, uint32_t sa,
-                                               uint32_t sb) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, I, (int)sa, I, (int)sb);
-}
+template <typename O>
+constexpr bool kFp8Exact = sizeof(O) == 4;
 
 __device__ __forceinline__ void f8_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void f8_put(bf16_t* p, float v) { *p = (bf16_t)bf16_bits(v); }
+
+__device__ __forceinline__ uint4 load16(const uint8_t* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
+
+// Bytes 4 g .. 4 g + 3 of a row of nkb scale bytes as a word, 127 past the
+// end.  No branches: a product loop that holds one is cut into blocks, and the
+// compiler then moves products across them and spills their accumulators.
+// Load and use are apart, so that a loop can wait for the bytes where it needs
+// them.
+struct Fp8ScaleBytes {
+  uint32_t b[4];
+};
+__device__ __forceinline__ Fp8ScaleBytes fp8_scale_load(const uint8_t* row, int g, int nkb) {
+  Fp8ScaleBytes s;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s.b[e] = row[min(4 * g + e, nkb - 1)];
+  return s;
+}
+__device__ __forceinline__ uint32_t fp8_scale_word(const Fp8ScaleBytes& s, int g, int nkb) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w |= (4 * g + e < nkb ? s.b[e] : 127u) << (8 * e);
+  return w;
+}
 
 // Few hidden rows: the weights are read straight into registers, once, and
 // the kernel is bound by them.  A workgroup owns 32 vocabulary rows and up to
@@ -164,7 +236,7 @@ __global__ __launch_bounds__(kF8Threads) void fp8_skinny_kernel(
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const size_t m = (size_t)min(m0 + 32 * t + l32, M - 1);   // rows past M repeat the last
-    hrow[t] = H + m * D + 64 * h;
+    hrow[t] = H + m * D + 32 * h;
     hsc[t] = hs + m * nkb;
   }
   fp8_f32x16 acc[MT];
@@ -177,16 +249,15 @@ __global__ __launch_bounds__(kF8Threads) void fp8_skinny_kernel(
     constexpr int I = decltype(idx)::value;
     uint4 a[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      a[s] = *reinterpret_cast<const uint4*>(wrow + (size_t)kb * kF8RunBytes + s * 1024);
+    for (int s = 0; s < 4; ++s) a[s] = load16(wrow + (size_t)kb * kF8RunBytes + s * 1024);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       uint4 b[4];
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        b[s] = *reinterpret_cast<const uint4*>(hrow[t] + kb * kFp8Block + 16 * s);
-      acc[t] = fp8_mfma<I>(fp8_operand(a[0], a[1]), fp8_operand(b[0], b[1]), acc[t], sa, sb[t]);
-      acc[t] = fp8_mfma<I>(fp8_operand(a[2], a[3]), fp8_operand(b[2], b[3]), acc[t], sa, sb[t]);
+        b[s] = load16(hrow[t] + kb * kFp8Block + 64 * (s / 2) + 16 * (s % 2));
+      acc[t] = fp8_step<kFp8Exact<O>, I>({a[0], a[1]}, {b[0], b[1]}, acc[t], sa, sb[t]);
+      acc[t] = fp8_step<kFp8Exact<O>, I>({a[2], a[3]}, {b[2], b[3]}, acc[t], sa, sb[t]);
     }
   };
   for (int g = wave; g < nk4; g += kF8Waves) {
@@ -194,12 +265,7 @@ __global__ __launch_bounds__(kF8Threads) void fp8_skinny_kernel(
     const int left = nkb - 4 * g;
     uint32_t sb[MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      sb[t] = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < left) sb[t] |= (uint32_t)hsc[t][4 * g + e] << (8 * e);
-    }
+    for (int t = 0; t < MT; ++t) sb[t] = fp8_scale_word(fp8_scale_load(hsc[t], g, nkb), g, nkb);
     run(std::integral_constant<int, 0>{}, 4 * g, sa, sb);
     if (left > 1) run(std::integral_constant<int, 1>{}, 4 * g + 1, sa, sb);
     if (left > 2) run(std::integral_constant<int, 2>{}, 4 * g + 2, sa, sb);
@@ -221,16 +287,241 @@ __global__ __launch_bounds__(kF8Threads) void fp8_skinny_kernel(
   }
 }
 
+// LDS writes of this workgroup made visible at a barrier, global loads left
+// in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Many hidden rows.  A workgroup of four waves owns 256 vocabulary rows (64 a
+// wave) and 32 MT hidden rows; two workgroups share a CU and cover each
+// other's waits.  Each wave reads its weights straight into registers, a run
+// ahead; the hidden rows of a run are staged in LDS, a run ahead, and every
+// wave reads all of them, each fragment feeding two products (64 vocabulary
+// rows a wave halve the LDS reads of 32).  The products of kPin fragments are
+// kept together (sched_barrier), the compiler orders them.
+//
+// Rows of a staged run are 128 bytes, their eight 16-byte pieces swapped by
+// row pair (row r's piece p at slot p ^ ((r >> 1) & 7)), so that 16
+// consecutive rows cover every bank once.
+//
+// Workgroups are numbered so that one XCD (every eighth block) takes
+// consecutive (vocabulary tile, row block) pairs, row blocks first: the
+// blocks that share weights run side by side under one L2.
+constexpr int kTileVocab = 256;
+constexpr int kTileGroups = kTileVocab / kF8Group;
+constexpr int kXcds = 8;
+constexpr int kPin = 4;
+static_assert(kTileGroups == 2 * kF8Waves, "two packed groups to a wave");
+
+template <int MT, typename O>
+__global__ __launch_bounds__(kF8Threads, 2) void fp8_tile_kernel(
+    const uint8_t* __restrict__ H, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ P,
+    const uint32_t* __restrict__ ws, int M, int D, int V, int ngroup, int nrb, int nwork,
+    O* __restrict__ out) {
+  constexpr int kRows = MT * 32;
+  constexpr int kBuf = kRows * kFp8Block;
+  constexpr int kTrStride = kTileVocab + 8;                 // epilogue rows, bfloat16
+  static_assert(kRows <= kF8Threads, "one row's scales to a thread");
+  static_assert(2 * kBuf >= 32 * kTrStride * (int)sizeof(bf16_t), "the epilogue reuses the buffers");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuf];
+  __shared__ uint32_t lsc[2][kF8Threads];                    // words past kRows are not read
+
+  const int per = (nwork + kXcds - 1) / kXcds;
+  const int work = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
+  if (work >= nwork) return;                                 // blockIdx.x / kXcds < per
+  const int tile = work / nrb, m0 = (work % nrb) * kRows;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int h = lane / 32, l32 = lane % 32;
+  const int nkb = D / kFp8Block, nk4 = (nkb + 3) / 4;
+
+  // this wave's two packed groups; groups past V repeat the last (dropped)
+  const int g0 = min(tile * kTileGroups + wave * 2, ngroup - 1), g1 = min(g0 + 1, ngroup - 1);
+  const uint8_t* w0 = P + (size_t)g0 * nkb * kF8RunBytes;
+  const uint8_t* w1 = P + (size_t)g1 * nkb * kF8RunBytes;
+  const uint32_t* s0 = ws + (size_t)g0 * nk4 * kF8Group;
+  const uint32_t* s1 = ws + (size_t)g1 * nk4 * kF8Group;
+  const uint32_t lane16 = lane * 16;
+
+  // staging: this thread's pieces are tid + 256 j, eight to a row; rows past
+  // M repeat the last (dropped)
+  const uint8_t* hb = H + (size_t)m0 * D;
+  const int left = M - 1 - m0;
+  uint32_t hoff[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+    hoff[j] = (uint32_t)min(tid / 8 + 32 * j, left) * D + (tid % 8) * 16;
+  const int slot = (tid / 8) * kFp8Block + (((tid % 8) ^ ((tid / 16) & 7)) * 16);
+  const uint8_t* hsrow = hs + (size_t)(m0 + min(tid, left)) * nkb;
+
+  fp8_f32x16 acc[2][MT];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][t][r] = 0.f;
+
+  uint4 wr[2][2][4], st[MT];
+  auto load_w = [&](int kb, uint4 (&d)[2][4]) {             // past the end: the last run again
+    const size_t at = (size_t)min(kb, nkb - 1) * kF8RunBytes;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      d[0][s] = load16(w0 + at + lane16 + s * 1024);
+      d[1][s] = load16(w1 + at + lane16 + s * 1024);
+    }
+  };
+  auto load_h = [&](int kb) {
+    const uint8_t* src = hb + (size_t)min(kb, nkb - 1) * kFp8Block;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) st[j] = load16(src + hoff[j]);
+  };
+  auto store_h = [&](int kb, int b) {                       // zeros past the end
+    const uint32_t keep = kb < nkb ? 0xffffffffu : 0u;
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      *reinterpret_cast<uint4*>(lds + b * kBuf + slot + j * 32 * kFp8Block) =
+          make_uint4(st[j].x & keep, st[j].y & keep, st[j].z & keep, st[j].w & keep);
+  };
+
+  uint32_t sa0 = s0[l32], sa1 = s1[l32], sb[MT];
+  load_h(0);
+  lsc[0][tid] = fp8_scale_word(fp8_scale_load(hsrow, 0, nkb), 0, nkb);
+  load_w(0, wr[0]);
+  store_h(0, 0);
+  lds_barrier();
+
+  auto run = [&](auto idx, int kb) {
+    constexpr int I = decltype(idx)::value;
+    load_h(kb + 1);
+    load_w(kb + 1, wr[(I + 1) % 2]);
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* buf = lds + (I % 2) * kBuf + l32 * kFp8Block;
+    const uint4(&w)[2][4] = wr[I % 2];
+    const int sw = (l32 >> 1) & 7;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const Fp8Bytes b = {load16(buf + t * 32 * kFp8Block + (((4 * s + 2 * h) ^ sw) * 16)),
+                            load16(buf + t * 32 * kFp8Block + (((4 * s + 2 * h + 1) ^ sw) * 16))};
+        acc[0][t] = fp8_step<kFp8Exact<O>, I>({w[0][2 * s], w[0][2 * s + 1]}, b, acc[0][t], sa0, sb[t]);
+        acc[1][t] = fp8_step<kFp8Exact<O>, I>({w[1][2 * s], w[1][2 * s + 1]}, b, acc[1][t], sa1, sb[t]);
+        if ((s * MT + t) % kPin == kPin - 1) __builtin_amdgcn_sched_barrier(0);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    store_h(kb + 1, (I + 1) % 2);
+  };
+  // groups of four runs, one scale word; runs past the last multiply zeros
+  for (int g = 0; g < nk4; ++g) {
+    const int next = min(g + 1, nk4 - 1);
+    const uint32_t n0 = s0[next * kF8Group + l32], n1 = s1[next * kF8Group + l32];
+    const Fp8ScaleBytes nh = fp8_scale_load(hsrow, next, nkb);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) sb[t] = lsc[g & 1][t * 32 + l32];
+    run(std::integral_constant<int, 0>{}, 4 * g);
+    lds_barrier();
+    run(std::integral_constant<int, 1>{}, 4 * g + 1);
+    lds_barrier();
+    run(std::integral_constant<int, 2>{}, 4 * g + 2);
+    lds_barrier();
+    run(std::integral_constant<int, 3>{}, 4 * g + 3);
+    lsc[(g + 1) & 1][tid] = fp8_scale_word(nh, next, nkb);
+    lds_barrier();
+    sa0 = n0;
+    sa1 = n1;
+  }
+
+  // acc[a][t][r] is the logit of row 32 t + l32 of the block and vocabulary id
+  // 64 wave + 32 a + 8 (r / 4) + r % 4 + 4 h of the tile.
+  const int vb = wave * 64 + 4 * h;
+  const int v0 = tile * kTileVocab;
+  const bool whole = V % (16 / sizeof(O)) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+  if constexpr (sizeof(O) == 2) {
+    if (whole) {
+      // 32 rows at a time through LDS, so that the stores cover whole 512-byte
+      // row segments
+      bf16_t* tr = reinterpret_cast<bf16_t*>(lds);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint2 w;
+            w.x = bf16_bits(acc[a][t][4 * q]) | bf16_bits(acc[a][t][4 * q + 1]) << 16;
+            w.y = bf16_bits(acc[a][t][4 * q + 2]) | bf16_bits(acc[a][t][4 * q + 3]) << 16;
+            *reinterpret_cast<uint2*>(tr + l32 * kTrStride + vb + 32 * a + 8 * q) = w;
+          }
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int p = tid + i * kF8Threads, row = p / 32, c = (p % 32) * 8;
+          if (m0 + t * 32 + row < M && v0 + c < V)
+            *reinterpret_cast<uint4*>(out + (size_t)(m0 + t * 32 + row) * V + v0 + c) =
+                *reinterpret_cast<const uint4*>(tr + row * kTrStride + c);
+        }
+        lds_barrier();
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = m0 + t * 32 + l32;
+    if (m >= M) continue;
+    O* row = out + (size_t)m * V;
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int v = v0 + vb + 32 * a + 8 * q;
+        if constexpr (sizeof(O) == 4) {
+          if (whole && v < V) {                             // V a multiple of 4: v + 3 < V too
+            *reinterpret_cast<float4*>(row + v) =
+                make_float4(acc[a][t][4 * q], acc[a][t][4 * q + 1], acc[a][t][4 * q + 2],
+                            acc[a][t][4 * q + 3]);
+            continue;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (v + i < V) f8_put(row + v + i, acc[a][t][4 * q + i]);
+      }
+  }
+}
+
+template <int MT, typename O>
+hipError_t fp8_tiles(const uint8_t* H, const uint8_t* hs, const uint8_t* P, const uint32_t* ws,
+                     int M, int D, int V, O* out, hipStream_t stream) {
+  const int nrb = (M + 32 * MT - 1) / (32 * MT);
+  const size_t nwork = (size_t)((V + kTileVocab - 1) / kTileVocab) * nrb;
+  const size_t blocks = (nwork + kXcds - 1) / kXcds * kXcds;
+  if (blocks > 0x7fffffffu) return hipErrorInvalidConfiguration;
+  fp8_tile_kernel<MT, O><<<dim3((unsigned)blocks), dim3(kF8Threads), 0, stream>>>(
+      H, hs, P, ws, M, D, V, fp8_groups(V), nrb, (int)nwork, out);
+  return hipGetLastError();
+}
+
 template <typename O>
 hipError_t fp8_head(const uint8_t* H, const uint8_t* hs, const uint8_t* P, int M, int D, int V,
                     O* out, hipStream_t stream) {
   const uint32_t* ws = reinterpret_cast<const uint32_t*>(P + fp8_packed_scale_off(V, D));
   const int ng = fp8_groups(V);
-  const int mt = M <= 32 ? 1 : 2;
-  const size_t blocks = (size_t)ng * ((M + 32 * mt - 1) / (32 * mt));
-  if (blocks > 0x7fffffffu) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks), thr(kF8Threads);
-  if (mt == 1) fp8_skinny_kernel<1, O><<<grid, thr, 0, stream>>>(H, hs, P, ws, M, D, V, ng, out);
+  if (M > 64) {
+    // row blocks of 96 where they leave fewer rows empty, else of 128 (669 vs
+    // 714 us at 1152 x 152064 x 4096).  Float32 logits always take 96: the
+    // wider operands would spill at 128.
+    if constexpr (!kFp8Exact<O>)
+      if ((M + 127) / 128 * 128 <= (M + 95) / 96 * 96)
+        return fp8_tiles<4, O>(H, hs, P, ws, M, D, V, out, stream);
+    return fp8_tiles<3, O>(H, hs, P, ws, M, D, V, out, stream);
+  }
+  const dim3 grid((unsigned)ng), thr(kF8Threads);
+  if (M <= 32) fp8_skinny_kernel<1, O><<<grid, thr, 0, stream>>>(H, hs, P, ws, M, D, V, ng, out);
   else fp8_skinny_kernel<2, O><<<grid, thr, 0, stream>>>(H, hs, P, ws, M, D, V, ng, out);
   return hipGetLastError();
 }

@@ -13,21 +13,23 @@ the library is not built the calls raise: there is no fallback.
 ``torch.float8_e8m0fnu`` scale [..., D / 128] for each run of 128.
 """
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 
 import torch
 
 from . import binding
-from .binding import SPECV_BF16, SPECV_EINVAL, SPECV_OK, SpecVerifyError, _check, _ptr
+from .binding import SPECV_EINVAL, SPECV_OK, SpecVerifyError, _check
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspecverify_ops.so")
 
 FP8_BLOCK = 128
 E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
-_OUT_CODES = {torch.float32: 0, torch.bfloat16: 1, E4M3: 2}
+_VALUE_CODES = {torch.float32: 0, torch.bfloat16: 1}
+_OUT_CODES = {**_VALUE_CODES, E4M3: 2}
+_ANY_DIMS = (1, 2, 3, 4)
 
 _lib = None
 _lock = threading.Lock()
@@ -40,6 +42,8 @@ def ops_library_path():
 def load_ops_library():
     """Load libspecverify_ops.so and declare its C signatures (once)."""
     global _lib
+    if _lib is not None:
+        return _lib
     binding.load_library()
     with _lock:
         if _lib is not None:
@@ -81,14 +85,18 @@ class _Call:
     """Device and stream of one call: allocations made for it are kept from
     reuse until the stream has run it, whichever stream is current."""
 
+    __slots__ = ("dev", "stream", "other", "ptr")
+
     def __init__(self, dev, stream):
-        current = torch.cuda.current_stream(dev)
         self.dev = dev
-        self.stream = current if stream is None else stream
-        if self.stream.device != dev:
-            raise ValueError(f"stream is on {self.stream.device}, the tensors on {dev}")
-        self.other = self.stream != current
-        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
+        self.ptr = torch._C._cuda_getCurrentRawStream(dev.index)
+        self.other = False
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+            self.other = stream.cuda_stream != self.ptr
+            self.ptr = stream.cuda_stream
+        self.stream = stream
 
     def empty(self, shape, dtype):
         t = torch.empty(shape, dtype=dtype, device=self.dev)
@@ -97,35 +105,50 @@ class _Call:
         return t
 
     def zeros(self, nbytes):
+        if not self.other:
+            return torch.zeros(nbytes, dtype=torch.uint8, device=self.dev)
         with torch.cuda.stream(self.stream):
             t = torch.zeros(nbytes, dtype=torch.uint8, device=self.dev)
-        if self.other:
-            t.record_stream(torch.cuda.current_stream(self.dev))
+        t.record_stream(torch.cuda.current_stream(self.dev))
         return t
 
-    def device(self):
-        """The tensors' device made current, where it is not."""
-        if self.dev.index == torch.cuda.current_device():
-            return contextlib.nullcontext()
-        return torch.cuda.device(self.dev)
+    def run(self, f, *args):
+        """The library call ``f`` with the tensors' device current."""
+        if self.dev.index == torch._C._cuda_getDevice():
+            status = f(*args)
+        else:
+            with torch.cuda.device(self.dev):
+                status = f(*args)
+        if status != SPECV_OK:
+            raise SpecVerifyError(status, binding.status_string(status))
 
 
-def _done(status):
-    if status != SPECV_OK:
-        raise SpecVerifyError(status, binding.status_string(status))
+def _ptr(t):
+    return None if t is None else t.data_ptr() or None
+
+
+def _match(t, name, dtype, shape, dev):
+    """``binding._check`` with its answer for a tensor that passes first."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and \
+            t.device == dev and t.is_contiguous():
+        return
+    _check(t, name, dtype, shape, dev)
 
 
 def _gpu(t, name, dims):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda" or t.dim() not in dims:
+    if not t.is_cuda or t.dim() not in dims:
         raise ValueError(f"{name} must be a GPU tensor of {' or '.join(map(str, dims))} dimensions")
 
 
 def _value_code(t, name):
-    if t.dtype not in (torch.float32, torch.bfloat16):
+    code = _VALUE_CODES.get(getattr(t, "dtype", None))
+    if code is None:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
         raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    return _OUT_CODES[t.dtype]
+    return code
 
 
 def hidden_norm(x, residual, weight, *, post_weight=None, gate=None, scale=1.0, eps=1e-6,
@@ -143,46 +166,51 @@ def hidden_norm(x, residual, weight, *, post_weight=None, gate=None, scale=1.0, 
     needs D a multiple of 128.  ``residual_out`` may be ``residual``.
     Asynchronous on ``stream``."""
     lib = load_ops_library()
-    _gpu(x, "x", (1, 2, 3, 4))
-    dev, shape, D = x.device, tuple(x.shape), x.shape[-1]
+    _gpu(x, "x", _ANY_DIMS)
+    dev, shape = x.device, x.shape
+    D = shape[-1]
     M = x.numel() // D if D else 0
-    xc = _value_code(x, "x")
-    _check(x, "x", None, shape, dev)
-    rc = _value_code(residual, "residual")
-    _check(residual, "residual", None, shape, dev)
-    wc = _value_code(weight, "weight")
-    _check(weight, "weight", None, (D,), dev)
+    xc, rc, wc = _value_code(x, "x"), _value_code(residual, "residual"), _value_code(weight, "weight")
+    _match(x, "x", x.dtype, shape, dev)
+    _match(residual, "residual", residual.dtype, shape, dev)
+    _match(weight, "weight", weight.dtype, (D,), dev)
     if post_weight is not None:
-        _check(post_weight, "post_weight", weight.dtype, (D,), dev)
+        _match(post_weight, "post_weight", weight.dtype, (D,), dev)
     rows = 1
     if gate is not None:
         _gpu(gate, "gate", (1, 2))
-        rows = gate.shape[0] if gate.dim() == 2 else 1
-        _check(gate, "gate", weight.dtype, (rows, D) if gate.dim() == 2 else (D,), dev)
-        if rows < 1 or M % rows:
-            raise ValueError(f"gate has {rows} rows, which do not divide the {M} rows of x")
-    if dtype not in _OUT_CODES:
+        if gate.dim() == 2:
+            rows = gate.shape[0]
+            _match(gate, "gate", weight.dtype, (rows, D), dev)
+            if rows < 1 or M % rows:
+                raise ValueError(f"gate has {rows} rows, which do not divide the {M} rows of x")
+        else:
+            _match(gate, "gate", weight.dtype, (D,), dev)
+    code = _OUT_CODES.get(dtype)
+    if code is None:
         raise TypeError(f"dtype must be bfloat16, float32 or float8_e4m3fn, got {dtype}")
     call = _Call(dev, stream)
     if residual_out is None:
         residual_out = call.empty(shape, residual.dtype)
-    _check(residual_out, "residual_out", residual.dtype, shape, dev)
-    if out is None:
-        out = call.empty(shape, dtype)
-    _check(out, "out", dtype, shape, dev)
+    else:
+        _match(residual_out, "residual_out", residual.dtype, shape, dev)
     if dtype == E4M3:
         if D % FP8_BLOCK:
             raise ValueError(f"8-bit output needs D a multiple of {FP8_BLOCK}, got {D}")
+        sshape = shape[:-1] + (D // FP8_BLOCK,)
         if out_scale is None:
-            out_scale = call.empty(shape[:-1] + (D // FP8_BLOCK,), E8M0)
-        _check(out_scale, "out_scale", E8M0, shape[:-1] + (D // FP8_BLOCK,), dev)
+            out_scale = call.empty(sshape, E8M0)
+        else:
+            _match(out_scale, "out_scale", E8M0, sshape, dev)
     elif out_scale is not None:
         raise ValueError("out_scale goes with 8-bit output only")
-    with call.device():
-        _done(lib.specv_hidden_norm(_ptr(x), xc, _ptr(residual), rc, _ptr(post_weight), _ptr(gate),
-                                    rows, _ptr(weight), wc, M, D, float(scale), float(eps),
-                                    _ptr(residual_out), _ptr(out), _OUT_CODES[dtype],
-                                    _ptr(out_scale), call.ptr))
+    if out is None:
+        out = call.empty(shape, dtype)
+    else:
+        _match(out, "out", dtype, shape, dev)
+    call.run(lib.specv_hidden_norm, x.data_ptr(), xc, residual.data_ptr(), rc, _ptr(post_weight),
+             _ptr(gate), rows, weight.data_ptr(), wc, M, D, scale, eps, residual_out.data_ptr(),
+             out.data_ptr(), code, _ptr(out_scale), call.ptr)
     return (residual_out, out, out_scale) if dtype == E4M3 else (residual_out, out)
 
 
@@ -192,23 +220,25 @@ def quantize_fp8(x, *, out=None, out_scale=None, stream=None):
     x ~ q * scale with the smallest power of two that brings each run's
     largest magnitude to at most 448.  Asynchronous on ``stream``."""
     lib = load_ops_library()
-    _gpu(x, "x", (1, 2, 3, 4))
-    dev, shape, D = x.device, tuple(x.shape), x.shape[-1]
+    _gpu(x, "x", _ANY_DIMS)
+    dev, shape = x.device, x.shape
+    D = shape[-1]
     code = _value_code(x, "x")
-    _check(x, "x", None, shape, dev)
+    _match(x, "x", x.dtype, shape, dev)
     if D < 1 or D % FP8_BLOCK:
         raise ValueError(f"the last dimension must be a multiple of {FP8_BLOCK}, got {D}")
     call = _Call(dev, stream)
     sshape = shape[:-1] + (D // FP8_BLOCK,)
     if out is None:
         out = call.empty(shape, E4M3)
+    else:
+        _match(out, "out", E4M3, shape, dev)
     if out_scale is None:
         out_scale = call.empty(sshape, E8M0)
-    _check(out, "out", E4M3, shape, dev)
-    _check(out_scale, "out_scale", E8M0, sshape, dev)
-    with call.device():
-        _done(lib.specv_fp8_quantize(_ptr(x), code, x.numel() // D, D, _ptr(out), _ptr(out_scale),
-                                     call.ptr))
+    else:
+        _match(out_scale, "out_scale", E8M0, sshape, dev)
+    call.run(lib.specv_fp8_quantize, x.data_ptr(), code, x.numel() // D, D, out.data_ptr(),
+             out_scale.data_ptr(), call.ptr)
     return out, out_scale
 
 
@@ -220,6 +250,7 @@ class PackedFp8LmHead:
         self.data, self.V, self.D = data, int(V), int(D)
 
 
+@functools.lru_cache(maxsize=None)
 def fp8_lm_head_packed_weight_bytes(V, D):
     return int(load_ops_library().specv_fp8_lm_head_packed_weight_bytes(int(V), int(D)))
 
@@ -235,16 +266,15 @@ def pack_fp8_lm_head(weight, scale=None, *, stream=None):
     dev = weight.device
     if scale is None:
         weight, scale = quantize_fp8(weight, stream=stream)
-    _check(weight, "weight", E4M3, (V, D), dev)
+    _match(weight, "weight", E4M3, (V, D), dev)
     nbytes = fp8_lm_head_packed_weight_bytes(V, D)
     if nbytes == 0:
         raise SpecVerifyError(SPECV_EINVAL, f"unsupported LM-head shape V={V} D={D}")
-    _check(scale, "scale", E8M0, (V, D // FP8_BLOCK), dev)
+    _match(scale, "scale", E8M0, (V, D // FP8_BLOCK), dev)
     call = _Call(dev, stream)
     data = call.empty((nbytes,), torch.uint8)
-    with call.device():
-        _done(lib.specv_fp8_lm_head_pack_weight(_ptr(weight), _ptr(scale), _ptr(data), V, D,
-                                                call.ptr))
+    call.run(lib.specv_fp8_lm_head_pack_weight, weight.data_ptr(), scale.data_ptr(),
+             data.data_ptr(), V, D, call.ptr)
     return PackedFp8LmHead(data, V, D)
 
 
@@ -252,12 +282,12 @@ def _check_hidden(hidden, hidden_scale, packed, dims):
     _gpu(hidden, "hidden", dims)
     if not isinstance(packed, PackedFp8LmHead):
         raise TypeError("packed must be a PackedFp8LmHead")
-    dev, shape = hidden.device, tuple(hidden.shape)
+    dev, shape = hidden.device, hidden.shape
     if shape[-1] != packed.D:
         raise ValueError(f"packed weight has D={packed.D}, hidden D={shape[-1]}")
-    _check(hidden, "hidden", E4M3, shape, dev)
-    _check(hidden_scale, "hidden_scale", E8M0, shape[:-1] + (packed.D // FP8_BLOCK,), dev)
-    _check(packed.data, "packed", torch.uint8,
+    _match(hidden, "hidden", E4M3, shape, dev)
+    _match(hidden_scale, "hidden_scale", E8M0, shape[:-1] + (packed.D // FP8_BLOCK,), dev)
+    _match(packed.data, "packed", torch.uint8,
            (fp8_lm_head_packed_weight_bytes(packed.V, packed.D),), dev)
     return dev, shape
 
@@ -267,19 +297,53 @@ def fp8_lm_head(hidden, hidden_scale, packed, *, dtype=torch.bfloat16, logits=No
     float8_e4m3fn with their scales (``hidden_norm`` or ``quantize_fp8``) and a
     ``PackedFp8LmHead``; float32 accumulation.  Asynchronous on ``stream``."""
     lib = load_ops_library()
-    dev, shape = _check_hidden(hidden, hidden_scale, packed, (1, 2, 3, 4))
-    if dtype not in (torch.bfloat16, torch.float32):
+    dev, shape = _check_hidden(hidden, hidden_scale, packed, _ANY_DIMS)
+    code = _VALUE_CODES.get(dtype)
+    if code is None:
         raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
     call = _Call(dev, stream)
     oshape = shape[:-1] + (packed.V,)
     if logits is None:
         logits = call.empty(oshape, dtype)
-    _check(logits, "logits", dtype, oshape, dev)
-    with call.device():
-        _done(lib.specv_fp8_lm_head(_ptr(hidden), _ptr(hidden_scale), _ptr(packed.data),
-                                    hidden.numel() // packed.D, packed.D, packed.V, _ptr(logits),
-                                    _OUT_CODES[dtype], call.ptr))
+    else:
+        _match(logits, "logits", dtype, oshape, dev)
+    call.run(lib.specv_fp8_lm_head, hidden.data_ptr(), hidden_scale.data_ptr(),
+             packed.data.data_ptr(), hidden.numel() // packed.D, packed.D, packed.V,
+             logits.data_ptr(), code, call.ptr)
     return logits
+
+
+def _check_round(draft_tokens, draft_len, u, u_final, B, K, dev):
+    _match(draft_tokens, "draft_tokens", torch.int32, (B, K), dev)
+    _match(draft_len, "draft_len", torch.int32, (B,), dev)
+    _match(u, "u", torch.float32, (B, K), dev)
+    _match(u_final, "u_final", torch.float32, (B,), dev)
+
+
+def _outputs(call, B, K, out_tokens, n_emitted, debug):
+    """The result dict and the diagnostics' addresses."""
+    if out_tokens is None:
+        out_tokens = call.empty((B, K + 1), torch.int32)
+    else:
+        _match(out_tokens, "out_tokens", torch.int32, (B, K + 1), call.dev)
+    if n_emitted is None:
+        n_emitted = call.empty((B,), torch.int32)
+    else:
+        _match(n_emitted, "n_emitted", torch.int32, (B,), call.dev)
+    res = {"out_tokens": out_tokens, "n_emitted": n_emitted}
+    if not debug:
+        return res, (None, None, None, None)
+    diag = (call.empty((B, K), torch.float32), call.empty((B,), torch.float64),
+            call.empty((B,), torch.int32), call.empty((B,), torch.int32))
+    res.update(zip(("accept_prob", "residual_mass", "stop_pos", "path"), diag))
+    return res, tuple(_ptr(t) for t in diag)
+
+
+def _space(workspace, dev):
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or \
+            not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
 def verify_fp8_lm_head(hidden, hidden_scale, packed, draft_logits, draft_tokens, draft_len, u,
@@ -293,17 +357,15 @@ def verify_fp8_lm_head(hidden, hidden_scale, packed, draft_logits, draft_tokens,
     lib = load_ops_library()
     dev, (B, K1, D) = _check_hidden(hidden, hidden_scale, packed, (3,))
     K, V, bf = K1 - 1, packed.V, torch.bfloat16
-    _check(draft_logits, "draft_logits", bf, (B, K, V), dev)
-    _check(draft_tokens, "draft_tokens", torch.int32, (B, K), dev)
-    _check(draft_len, "draft_len", torch.int32, (B,), dev)
-    _check(u, "u", torch.float32, (B, K), dev)
-    _check(u_final, "u_final", torch.float32, (B,), dev)
+    _match(draft_logits, "draft_logits", bf, (B, K, V), dev)
+    _check_round(draft_tokens, draft_len, u, u_final, B, K, dev)
     call = _Call(dev, stream)
     if target_logits is None:
-        target_logits = call.empty((B, K + 1, V), bf)
-    _check(target_logits, "target_logits", bf, (B, K + 1, V), dev)
-    res = {"target_logits": target_logits}
-    res.update(_outputs(call, B, K, out_tokens, n_emitted, debug))
+        target_logits = call.empty((B, K1, V), bf)
+    else:
+        _match(target_logits, "target_logits", bf, (B, K1, V), dev)
+    res, diag = _outputs(call, B, K, out_tokens, n_emitted, debug)
+    res["target_logits"] = target_logits
     if workspace is None:
         nbytes = int(lib.specv_verify_fp8_lm_head_workspace_bytes(B, K, V, D, int(top_k),
                                                                   float(top_p)))
@@ -316,41 +378,12 @@ def verify_fp8_lm_head(hidden, hidden_scale, packed, draft_logits, draft_tokens,
             workspace = call.zeros(nbytes)
         else:
             workspace = call.empty((nbytes,), torch.uint8)
-    with call.device():
-        _done(lib.specv_verify_fp8_lm_head(
-            _ptr(hidden), _ptr(hidden_scale), _ptr(packed.data), _ptr(draft_logits),
-            _ptr(draft_tokens), _ptr(draft_len), _ptr(u), _ptr(u_final), B, K, V, D,
-            float(temperature), int(top_k), float(top_p), int(eos_id), _ptr(target_logits),
-            _ptr(res["out_tokens"]), _ptr(res["n_emitted"]), *_space(workspace, dev), call.ptr,
-            *_diagnostics(res)))
+    call.run(lib.specv_verify_fp8_lm_head, _ptr(hidden), _ptr(hidden_scale), _ptr(packed.data),
+             _ptr(draft_logits), _ptr(draft_tokens), _ptr(draft_len), _ptr(u), _ptr(u_final), B, K,
+             V, D, float(temperature), int(top_k), float(top_p), int(eos_id), _ptr(target_logits),
+             _ptr(res["out_tokens"]), _ptr(res["n_emitted"]), *_space(workspace, dev), call.ptr,
+             *diag)
     return res
-
-
-def _outputs(call, B, K, out_tokens, n_emitted, debug):
-    if out_tokens is None:
-        out_tokens = call.empty((B, K + 1), torch.int32)
-    if n_emitted is None:
-        n_emitted = call.empty((B,), torch.int32)
-    _check(out_tokens, "out_tokens", torch.int32, (B, K + 1), call.dev)
-    _check(n_emitted, "n_emitted", torch.int32, (B,), call.dev)
-    res = {"out_tokens": out_tokens, "n_emitted": n_emitted}
-    if debug:
-        res["accept_prob"] = call.empty((B, K), torch.float32)
-        res["residual_mass"] = call.empty((B,), torch.float64)
-        res["stop_pos"] = call.empty((B,), torch.int32)
-        res["path"] = call.empty((B,), torch.int32)
-    return res
-
-
-def _diagnostics(res):
-    return [_ptr(res.get(k)) for k in ("accept_prob", "residual_mass", "stop_pos", "path")]
-
-
-def _space(workspace, dev):
-    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or \
-            not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
 def _rows(t, name, shape, dev):
@@ -359,13 +392,15 @@ def _rows(t, name, shape, dev):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.numel() and shape[2] > 1 and t.stride(2) != 1:
+    sb, sk, sv = t.stride()
+    if sv != 1 and shape[2] > 1 and t.numel():
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.stride(0), t.stride(1)
+    return sb, sk
 
 
+@functools.lru_cache(maxsize=1024)
 def verify_probs_workspace_bytes(B, K, V):
     return int(load_ops_library().specv_verify_probs_workspace_bytes(int(B), int(K), int(V)))
 
@@ -394,17 +429,13 @@ def verify_probs(target_probs, draft_probs, draft_tokens, draft_len, u, u_final,
         dsb, dsk = _rows(draft_probs, "draft_probs", (B, K, V), dev)
         if draft_probs.dtype != target_probs.dtype:
             raise TypeError(f"draft_probs must be {target_probs.dtype}, got {draft_probs.dtype}")
-    _check(draft_tokens, "draft_tokens", torch.int32, (B, K), dev)
-    _check(draft_len, "draft_len", torch.int32, (B,), dev)
-    _check(u, "u", torch.float32, (B, K), dev)
-    _check(u_final, "u_final", torch.float32, (B,), dev)
+    _check_round(draft_tokens, draft_len, u, u_final, B, K, dev)
     call = _Call(dev, stream)
-    res = _outputs(call, B, K, out_tokens, n_emitted, debug)
+    res, diag = _outputs(call, B, K, out_tokens, n_emitted, debug)
     if workspace is None:
         workspace = call.empty((verify_probs_workspace_bytes(B, K, V),), torch.uint8)
-    with call.device():
-        _done(lib.specv_verify_probs(
-            _ptr(target_probs), tsb, tsk, _ptr(draft_probs), dsb, dsk, code, _ptr(draft_tokens),
-            _ptr(draft_len), _ptr(u), _ptr(u_final), B, K, V, int(eos_id), _ptr(res["out_tokens"]),
-            _ptr(res["n_emitted"]), *_space(workspace, dev), call.ptr, *_diagnostics(res)))
+    call.run(lib.specv_verify_probs, _ptr(target_probs), tsb, tsk, _ptr(draft_probs), dsb, dsk,
+             code, _ptr(draft_tokens), _ptr(draft_len), _ptr(u), _ptr(u_final), B, K, V, eos_id,
+             _ptr(res["out_tokens"]), _ptr(res["n_emitted"]), *_space(workspace, dev), call.ptr,
+             *diag)
     return res
