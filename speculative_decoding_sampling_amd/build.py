@@ -4,7 +4,8 @@ Usage: ``python -m speculative_decoding_sampling_amd.build`` (or
 ``__graft_entry__.build()``).  Compiles every source under ``csrc/`` to an
 object in ``_build/`` in parallel and links the two shared libraries next to
 this file, where the Python bindings load them.  libspecverify_ops calls
-libspecverify's public entry points and finds it in its own folder.
+libspecverify's public entry points and finds it in its own folder; the Python
+module _ops_native (host C++, torch's headers) calls libspecverify_ops.
 """
 
 import os
@@ -26,6 +27,9 @@ SOURCES = ["specverify.hip", "row_stats.hip", "accept.hip", "sample.hip", "filte
            "filter_rows.hip", "sample_list.hip", "diagnostics.hip", "round_policy.hip",
            "lm_head.hip", "small.hip"]
 OPS_SOURCES = ["ops.hip", "probs.hip", "hidden_norm.hip", "fp8_head.hip"]
+# Python module of the operators, host C++ against torch's headers
+OPS_EXT = os.path.join(HERE, "_ops_native.so")
+OPS_EXT_SOURCE = "ops_ext.cpp"
 # Packed FP32 instructions stay off: the compiler must not form v_pk_* FP32 ops.
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
@@ -62,16 +66,40 @@ def _link(hipcc, lib, sources, *extra):
     return out
 
 
+def _ext_commands():
+    """Compile and link command of the Python module."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cxx = shutil.which("g++") or "g++"
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [INCLUDE, "/opt/rocm/include", sysconfig.get_paths()["include"],
+           *cpp_extension.include_paths()]
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
+                "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                *[f"-isystem{d}" for d in inc], "-c", os.path.join(CSRC, OPS_EXT_SOURCE),
+                "-o", _object(OPS_EXT_SOURCE)]
+    link = [cxx, "-shared", "-o", OPS_EXT + ".tmp", _object(OPS_EXT_SOURCE), "-L", HERE,
+            "-lspecverify_ops", "-lspecverify", "-L", torch_lib, "-lc10", "-ltorch_cpu",
+            "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
 def build(verbose=False):
     hipcc = _hipcc()
     os.makedirs(BUILD, exist_ok=True)
+    ext_compile, ext_link = _ext_commands()
     cmds = [[hipcc, *FLAGS, "-c", os.path.join(CSRC, src), "-o", _object(src)]
-            for src in SOURCES + OPS_SOURCES]
+            for src in SOURCES + OPS_SOURCES] + [ext_compile]
     with ThreadPoolExecutor(max_workers=min(len(cmds), os.cpu_count() or 1, 8)) as ex:
         outs = list(ex.map(_run, cmds))
     outs.append(_link(hipcc, LIB, SOURCES))
     outs.append(_link(hipcc, OPS_LIB, OPS_SOURCES, "-L", HERE, "-lspecverify",
                       "-Wl,-rpath,$ORIGIN"))
+    outs.append(_run(ext_link))
+    os.replace(OPS_EXT + ".tmp", OPS_EXT)
     if verbose:
         for o in outs:
             if o.strip():

@@ -173,9 +173,12 @@ def test_python_calls_refuse_cpu_tensors(lib):
     x = torch.zeros(2, 128)
     for f in (lambda: S.hidden_norm(x, x, x[0]), lambda: S.quantize_fp8(x),
               lambda: S.pack_fp8_lm_head(x),
-              lambda: S.fp8_lm_head(x, x, None),
+              lambda: S.fp8_lm_head(x, x, S.PackedFp8LmHead(x, 2, 128)),
               lambda: S.verify_probs(x[None], None, None, None, None, None)):
         with pytest.raises(ValueError):
             f()
-    with pytest.raises(TypeError):
-        S.quantize_fp8([1.0])
+    for f in (lambda: S.quantize_fp8([1.0]), lambda: S.fp8_lm_head(x, x, None),
+              lambda: S.hidden_norm(x, x, x[0], dtype=torch.float16),
+              lambda: S.verify_probs(None, None, None, None, None, None)):
+        with pytest.raises(TypeError):
+            f()
