@@ -183,7 +183,8 @@ SPECV_OPS_API specv_status_t specv_verify_fp8_lm_head(
  *  draft_tokens, draft_len, u, u_final, eos_id, out_tokens, n_emitted: as for
  *                specv_verify.
  *  workspace     at least specv_verify_probs_workspace_bytes(B, K, V) bytes,
- *                16-byte aligned; needs no initialisation.
+ *                16-byte aligned; needs no initialisation.  A small V needs
+ *                none: the size is then 0 (as for sizes the call refuses).
  *  accept_prob, residual_mass, stop_pos, path: nullable diagnostics, as for
  *                specv_verify_debug.
  *

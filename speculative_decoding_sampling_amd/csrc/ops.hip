@@ -239,7 +239,8 @@ specv_status_t specv_verify_probs(const void* target_probs, int64_t target_strid
       misaligned(accept_prob, 4) || misaligned(residual_mass, 8) || misaligned(stop_pos, 4) ||
       misaligned(path, 4))
     return SPECV_EINVAL;
-  if (!workspace || misaligned(workspace, 16) || workspace_bytes < probs_workspace_bytes(B, V))
+  const size_t need = probs_workspace_bytes(B, V);
+  if (need > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
     return SPECV_EWORKSPACE;
   return status(launch_verify_probs(dtype == SPECV_BF16, target_probs, target_stride_b,
                                     target_stride_k, draft_probs, draft_stride_b, draft_stride_k,

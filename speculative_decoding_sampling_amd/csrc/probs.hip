@@ -16,8 +16,9 @@
 // Split.  A chunk is kProbChunk tokens, summed by one wave.  Each wave makes
 // the request's accept scan for itself (lane k owns position k, two dependent
 // loads) rather than wait for a scan kernel's plan: the scans run side by
-// side, a kernel boundary would not.  Then one wave per request walks the
-// chunk sums to the chunk that holds the draw and scans that chunk.  Small
+// side, a kernel boundary would not.  The wave of chunk 0 writes everything but
+// the drawn token, and the plan; then one wave per request walks the chunk
+// sums to the chunk that holds the draw and scans that chunk.  Small
 // vocabularies do both in one workgroup per request, the chunk sums in LDS.
 #include "common.h"
 #include "specverify.h"
@@ -34,11 +35,13 @@ constexpr int kProbOneChunks = 64;                 // LDS records of the one-ker
 static_assert(SPECV_MAX_V <= kProbChunk * kProbBatch * kWave,
               "one lane per batch of chunk records");
 
-// Sums over a chunk: w the weights the draw uses (the residual after a
-// rejection, p otherwise), p the target row.  NaN marks an invalid entry.
-struct ProbRec {
-  double w, p;
+// What the draw of a scanned request needs.
+struct ProbPlan {
+  int path, stop;
+  float uf;
+  int hot;            // the drafted token of a rejection without draft rows, else -1
 };
+static_assert(sizeof(ProbPlan) == 16, "ProbPlan is 16 bytes");
 
 struct ProbArgs {
   const void* tgt;
@@ -49,7 +52,8 @@ struct ProbArgs {
   const float* u;
   const float* u_final;
   int K, V, nch, eos_id;
-  ProbRec* recs;                    // [B][nch]
+  ProbPlan* plans;                  // [B]
+  double* recs;                     // [B][nch] chunk sums of the weights, NaN if invalid
   int* out_tokens;
   int* n_emitted;
   float* alpha_out;
@@ -115,33 +119,44 @@ __device__ __forceinline__ ProbScan prob_scan(const ProbArgs& a, int b, int lane
   return s;
 }
 
-// The rows the draw of a scanned request reads.
+__device__ __forceinline__ ProbPlan prob_plan(const ProbArgs& a, const ProbScan& s) {
+  ProbPlan p = {s.path, s.stop, s.uf, -1};
+  if (s.path == kPathReject && !a.dft) p.hot = lane_value(s.x, s.stop);
+  return p;
+}
+__device__ __forceinline__ bool prob_draws(int path) {
+  return path == kPathReject || path == kPathBonus;
+}
+
+// The rows the draw of a planned request reads.
 template <typename T>
 struct ProbRows {
   const T* p;
   const T* q;         // null: none, or one at token hot
-  int hot;            // the drafted token of a rejection without draft rows, else -1
+  int hot;
 };
 
 template <typename T>
-__device__ __forceinline__ ProbRows<T> prob_rows(const ProbArgs& a, int b, const ProbScan& s) {
+__device__ __forceinline__ ProbRows<T> prob_rows(const ProbArgs& a, int b, const ProbPlan& s) {
   ProbRows<T> r;
   r.p = static_cast<const T*>(a.tgt) + (size_t)b * a.tsb + (size_t)s.stop * a.tsk;
-  r.q = nullptr;
-  r.hot = -1;
-  if (s.path == kPathReject) {
-    if (a.dft) r.q = static_cast<const T*>(a.dft) + (size_t)b * a.dsb + (size_t)s.stop * a.dsk;
-    else r.hot = lane_value(s.x, s.stop);
-  }
+  r.q = s.path == kPathReject && a.dft
+            ? static_cast<const T*>(a.dft) + (size_t)b * a.dsb + (size_t)s.stop * a.dsk
+            : nullptr;
+  r.hot = s.hot;
   return r;
 }
 
-// The weight of one token; NaN for an invalid entry.
+// The weight of one token.  max(p - q, 0) of valid entries is p itself where
+// there is no q.
 __device__ __forceinline__ double prob_weight(float p, float q) {
-  const double d = (double)p - (double)q;
-  const double w = d > 0.0 ? d : 0.0;
-  return prob_ok(p) && prob_ok(q) ? w : __builtin_nan("");
+  return fmax((double)p - (double)q, 0.0);
 }
+
+// Validity of a batch of entries: the largest of their bits as unsigned
+// integers is below those of infinity unless one is negative, infinite or NaN
+// (or -0, which only the full test below tells).
+__device__ __forceinline__ uint32_t prob_bits(float p) { return __float_as_uint(p); }
 
 // 16 entries of a row as floats.  striped: entries base + (64 j + lane) N + i
 // (N per 16-byte vector, whole cache lines per load); otherwise the lane's
@@ -167,52 +182,68 @@ __device__ __forceinline__ void prob_load(const T* __restrict__ row, int base, i
   }
 }
 
-// Sums of chunk c, by one wave (every lane gets them).
+// Sum of chunk c's weights, by one wave (every lane gets it); NaN where an
+// entry is invalid.
 template <typename T>
-__device__ __forceinline__ ProbRec prob_chunk(const ProbRows<T>& r, int c, int lane, int V) {
+__device__ __forceinline__ double prob_chunk(const ProbRows<T>& r, int c, int lane, int V) {
   const int base = c * kProbChunk;
+  constexpr int N = Elem<T>::kPerVec;
   float p[kProbPer], q[kProbPer];
   prob_load<T, true>(r.p, base, lane, V, p);
-  if (r.q) prob_load<T, true>(r.q, base, lane, V, q);
-  else
+  const bool has_q = r.q || (r.hot >= base && r.hot < base + kProbChunk);   // uniform
+  if (r.q) {
+    prob_load<T, true>(r.q, base, lane, V, q);
+  } else {
 #pragma unroll
-    for (int i = 0; i < kProbPer; ++i) q[i] = 0.f;
-  constexpr int N = Elem<T>::kPerVec;
-  double w = 0.0, sp = 0.0;
+    for (int j = 0; j < kProbPer / N; ++j)
 #pragma unroll
-  for (int j = 0; j < kProbPer / N; ++j)
+      for (int i = 0; i < N; ++i) q[j * N + i] = base + (j * kWave + lane) * N + i == r.hot ? 1.f : 0.f;
+  }
+  uint32_t top = 0;
+  double w = 0.0;
+  if (has_q) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = j * N + i;
-      float qe = q[e];
-      if (base + (j * kWave + lane) * N + i == r.hot) qe = 1.f;
-      w += prob_weight(p[e], qe);
-      sp += (double)p[e];
+    for (int e = 0; e < kProbPer; ++e) {
+      top = max(top, max(prob_bits(p[e]), prob_bits(q[e])));
+      w += prob_weight(p[e], q[e]);
     }
-  ProbRec rec;
-  rec.w = wave_sum(w);
-  rec.p = wave_sum(sp);
-  return rec;
+  } else {
+#pragma unroll
+    for (int e = 0; e < kProbPer; ++e) {
+      top = max(top, prob_bits(p[e]));
+      w += (double)p[e];
+    }
+  }
+  if (top >= 0x7f800000u) {
+    bool ok = true;
+#pragma unroll
+    for (int e = 0; e < kProbPer; ++e) ok = ok && prob_ok(p[e]) && prob_ok(q[e]);
+    if (!ok) w = __builtin_nan("");
+  }
+  return wave_sum(w);
+}
+
+// The first lane whose running sum exceeds t, or where rounding leaves none
+// the last with a positive term.
+__device__ __forceinline__ int prob_lane(double incl, double term, double t) {
+  const uint64_t over = __ballot(incl > t && term > 0.0);
+  const uint64_t some = __ballot(term > 0.0);
+  return over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)some);
 }
 
 // The token of chunk c at t, base being the weights before the chunk: the
 // first whose running sum exceeds t, or where rounding leaves none the last
 // with a positive weight.
 template <typename T>
-__device__ __forceinline__ int prob_draw(const ProbRows<T>& r, int c, int lane, int V, bool use_p,
-                                         double base, double t) {
-  const int v0 = c * kProbChunk;
+__device__ __forceinline__ int prob_draw(const ProbRows<T>& r, int c, int lane, int V, double base,
+                                         double t) {
+  const int v0 = c * kProbChunk + lane * kProbPer;
   float p[kProbPer], q[kProbPer];
-  prob_load<T, false>(r.p, v0, lane, V, p);
-  if (r.q && !use_p) prob_load<T, false>(r.q, v0, lane, V, q);
+  prob_load<T, false>(r.p, c * kProbChunk, lane, V, p);
+  if (r.q) prob_load<T, false>(r.q, c * kProbChunk, lane, V, q);
   else
 #pragma unroll
-    for (int i = 0; i < kProbPer; ++i) q[i] = 0.f;
-  if (!use_p && r.hot >= v0 + lane * kProbPer && r.hot < v0 + (lane + 1) * kProbPer) {
-#pragma unroll
-    for (int i = 0; i < kProbPer; ++i)
-      if (v0 + lane * kProbPer + i == r.hot) q[i] = 1.f;
-  }
+    for (int i = 0; i < kProbPer; ++i) q[i] = v0 + i == r.hot ? 1.f : 0.f;
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < kProbPer; ++i) sum += prob_weight(p[i], q[i]);
@@ -226,70 +257,21 @@ __device__ __forceinline__ int prob_draw(const ProbRows<T>& r, int c, int lane, 
     if (first == kProbPer && run > t) first = i;
     if (w > 0.0) last = i;
   }
-  const uint64_t over = __ballot(base + incl > t && sum > 0.0);
-  const uint64_t some = __ballot(sum > 0.0);
-  const int L = over ? __ffsll((unsigned long long)over) - 1
-                     : some ? 63 - __clzll((long long)some) : 0;
-  const int pick = first < kProbPer && over ? first : last;
-  return v0 + L * kProbPer + lane_value(pick, L);
+  const int L = prob_lane(base + incl, sum, t) & (kWave - 1);
+  const int pick = first < kProbPer ? first : last;
+  return c * kProbChunk + L * kProbPer + lane_value(pick, L);
 }
 
-// The draw of a scanned request from its chunk records, and the request's
-// outputs, by one wave.
-template <typename T>
-__device__ __forceinline__ void prob_finish(const ProbArgs& a, int b, int lane, ProbScan s,
-                                            const ProbRec* recs) {
-  int y = -1;
-  double mass = 0.0;
-  if (s.path == kPathReject || s.path == kPathBonus) {
-    const ProbRows<T> rows = prob_rows<T>(a, b, s);
-    // lane i keeps the totals of record batch i
-    const int nbatch = (a.nch + kProbBatch - 1) / kProbBatch;
-    double bw = 0.0, bp = 0.0;
-    for (int i = 0; i < nbatch; ++i) {
-      const int c = i * kProbBatch + lane;
-      ProbRec r = {0.0, 0.0};
-      if (c < a.nch) r = recs[c];
-      const double sw = wave_sum(r.w), sp = wave_sum(r.p);
-      if (lane == i) {
-        bw = sw;
-        bp = sp;
-      }
-    }
-    const double W = wave_sum(bw), P = wave_sum(bp);
-    if (s.path == kPathReject) mass = W;
-    // an empty residual: the correction is drawn from p itself
-    const bool use_p = s.path == kPathReject && W == 0.0;
-    const double total = use_p ? P : W;
-    if (!(total > 0.0) || !(W >= 0.0)) {                   // zero or NaN
-      s.path = kPathError;
-    } else {
-      const double t = (double)s.uf * total;
-      const double bt = use_p ? bp : bw;
-      const double bincl = wave_incl_scan(bt);
-      const uint64_t bover = __ballot(bincl > t && bt > 0.0);
-      const uint64_t bsome = __ballot(bt > 0.0);
-      const int bi = bover ? __ffsll((unsigned long long)bover) - 1
-                           : 63 - __clzll((long long)bsome);
-      const double before = lane_value(wave_shr1(bincl), bi);
-      const int c = bi * kProbBatch + lane;
-      ProbRec r = {0.0, 0.0};
-      if (c < a.nch) r = recs[c];
-      const double ct = use_p ? r.p : r.w;
-      const double cincl = before + wave_incl_scan(ct);
-      const uint64_t cover = __ballot(cincl > t && ct > 0.0);
-      const uint64_t csome = __ballot(ct > 0.0);
-      const int ci = cover ? __ffsll((unsigned long long)cover) - 1
-                           : 63 - __clzll((long long)csome);
-      const double base = ci ? lane_value(cincl, ci - 1) : before;
-      y = prob_draw<T>(rows, bi * kProbBatch + ci, lane, a.V, use_p, base, t);
-    }
-  }
+// The outputs of a scanned request by one wave: y the drawn token, mass the
+// residual's.
+__device__ __forceinline__ void prob_outputs(const ProbArgs& a, int b, int lane,
+                                             const ProbScan& s, int y, double mass) {
   const bool err = s.path == kPathError;
   for (int k = lane; k <= a.K; k += kWave) {
     int v = -1;
     if (!err) {
-      if (k < s.stop || (k == s.stop && s.path == kPathEos)) v = s.x;   // k = lane < 64 here
+      // a position before the stop is one of the first 64: k = lane there
+      if (k < s.stop || (k == s.stop && s.path == kPathEos)) v = s.x;
       else if (k == s.stop) v = y;
     }
     a.out_tokens[(size_t)b * (a.K + 1) + k] = v;
@@ -303,6 +285,76 @@ __device__ __forceinline__ void prob_finish(const ProbArgs& a, int b, int lane, 
     if (a.path_out) a.path_out[b] = s.path;
   }
 }
+__device__ __forceinline__ void prob_error(const ProbArgs& a, int b, int lane) {
+  ProbScan e = {};
+  e.path = kPathError;
+  prob_outputs(a, b, lane, e, -1, 0.0);
+}
+
+// A walk over chunk sums, 64 at a time: rec(c), called by the whole wave, is
+// lane l's sum of chunk c = 64 i + l (0 past the last).  Lane i keeps the total
+// of batch i.
+struct ProbWalk {
+  double batch, total;
+};
+template <typename F>
+__device__ __forceinline__ ProbWalk prob_total(int nch, int lane, F rec) {
+  double mine = 0.0;
+  for (int i = 0; i * kProbBatch < nch; ++i) {
+    const double s = wave_sum(rec(i * kProbBatch + lane));
+    if (lane == i) mine = s;
+  }
+  return {mine, wave_sum(mine)};
+}
+// The chunk that holds t and the weights before it (total > 0).
+template <typename F>
+__device__ __forceinline__ int prob_find(const ProbWalk& w, int lane, double t, F rec,
+                                         double& before) {
+  const double bincl = wave_incl_scan(w.batch);
+  const int bi = prob_lane(bincl, w.batch, t);
+  const double start = lane_value(wave_shr1(bincl), bi);
+  const double r = rec(bi * kProbBatch + lane);
+  const double cincl = start + wave_incl_scan(r);
+  const int ci = prob_lane(cincl, r, t);
+  before = ci ? lane_value(cincl, ci - 1) : start;
+  return bi * kProbBatch + ci;
+}
+
+// The draw of a planned request from its chunk records, by one wave: the
+// token, -1 where an entry is invalid or there is no mass.
+template <typename T>
+__device__ __forceinline__ int prob_pick(const ProbArgs& a, int b, int lane, const ProbPlan& s,
+                                         const double* recs, double& mass) {
+  ProbRows<T> rows = prob_rows<T>(a, b, s);
+  double before;
+  auto rec = [&](int c) { return c < a.nch ? recs[c] : 0.0; };
+  const ProbWalk w = prob_total(a.nch, lane, rec);
+  mass = s.path == kPathReject ? w.total : 0.0;
+  if (w.total > 0.0) {
+    const double t = (double)s.uf * w.total;
+    const int c = prob_find(w, lane, t, rec, before);
+    return prob_draw<T>(rows, c, lane, a.V, before, t);
+  }
+  if (!(w.total == 0.0) || s.path != kPathReject) return -1;
+  // An empty residual: the correction is drawn from p itself, whose chunks
+  // this wave sums on the spot (only the rounding of the caller's
+  // probabilities leads here).
+  rows.q = nullptr;
+  rows.hot = -1;
+  auto sum = [&](int c) {
+    double mine = 0.0;
+    for (int l = 0; l < kProbBatch && c - lane + l < a.nch; ++l) {
+      const double v = prob_chunk<T>(rows, c - lane + l, lane, a.V);
+      if (lane == l) mine = v;
+    }
+    return mine;
+  };
+  const ProbWalk wp = prob_total(a.nch, lane, sum);
+  if (!(wp.total > 0.0)) return -1;
+  const double t = (double)s.uf * wp.total;
+  const int c = prob_find(wp, lane, t, sum, before);
+  return prob_draw<T>(rows, c, lane, a.V, before, t);
+}
 
 // Chunk sums: one wave per (request, chunk).
 template <typename T>
@@ -312,43 +364,73 @@ __global__ __launch_bounds__(kProbPassThreads) void prob_pass_kernel(ProbArgs a,
   const int lane = threadIdx.x % kWave;
   if (c >= a.nch) return;
   const ProbScan s = prob_scan<T>(a, b, lane);
-  if (s.path != kPathReject && s.path != kPathBonus) return;
-  const ProbRec r = prob_chunk<T>(prob_rows<T>(a, b, s), c, lane, a.V);
-  if (lane == 0) a.recs[(size_t)b * a.nch + c] = r;
+  const ProbPlan p = prob_plan(a, s);
+  if (prob_draws(s.path)) {
+    const double w = prob_chunk<T>(prob_rows<T>(a, b, p), c, lane, a.V);
+    if (lane == 0) a.recs[(size_t)b * a.nch + c] = w;
+  }
+  if (c == 0) {
+    prob_outputs(a, b, lane, s, -1, 0.0);
+    if (lane == 0) a.plans[b] = p;
+  }
 }
 
 // The draws: one wave per request.
 template <typename T>
 __global__ __launch_bounds__(kWave) void prob_draw_kernel(ProbArgs a) {
   const int b = blockIdx.x, lane = threadIdx.x;
-  const ProbScan s = prob_scan<T>(a, b, lane);
-  prob_finish<T>(a, b, lane, s, a.recs + (size_t)b * a.nch);
+  const ProbPlan p = a.plans[b];
+  if (!prob_draws(p.path)) return;
+  double mass;
+  const int y = prob_pick<T>(a, b, lane, p, a.recs + (size_t)b * a.nch, mass);
+  if (y < 0) {
+    prob_error(a, b, lane);
+  } else if (lane == 0) {
+    a.out_tokens[(size_t)b * (a.K + 1) + p.stop] = y;
+    if (a.rmass_out) a.rmass_out[b] = mass;
+  }
 }
 
 // Both in one workgroup per request.
 template <typename T>
 __global__ __launch_bounds__(kProbOneThreads) void prob_one_kernel(ProbArgs a) {
-  __shared__ ProbRec recs[kProbOneChunks];
+  __shared__ double recs[kProbOneChunks];
   const int b = blockIdx.x, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const ProbScan s = prob_scan<T>(a, b, lane);
-  if (s.path == kPathReject || s.path == kPathBonus) {
-    const ProbRows<T> rows = prob_rows<T>(a, b, s);
+  const ProbPlan p = prob_plan(a, s);
+  if (prob_draws(s.path)) {
+    const ProbRows<T> rows = prob_rows<T>(a, b, p);
     for (int c = wave; c < a.nch; c += kProbOneThreads / kWave) {
-      const ProbRec r = prob_chunk<T>(rows, c, lane, a.V);
-      if (lane == 0) recs[c] = r;
+      const double w = prob_chunk<T>(rows, c, lane, a.V);
+      if (lane == 0) recs[c] = w;
     }
   }
   __syncthreads();
-  if (wave == 0) prob_finish<T>(a, b, lane, s, recs);
+  if (wave != 0) return;
+  int y = -1;
+  double mass = 0.0;
+  if (prob_draws(s.path)) {
+    y = prob_pick<T>(a, b, lane, p, recs, mass);
+    if (y < 0) {
+      prob_error(a, b, lane);
+      return;
+    }
+  }
+  prob_outputs(a, b, lane, s, y, mass);
 }
 
 // Largest vocabulary the one-kernel form takes.
-constexpr int kProbOneV = 32768;
+#ifndef SPECV_ONE_V
+#define SPECV_ONE_V 32768
+#endif
+constexpr int kProbOneV = SPECV_ONE_V;
 static_assert(kProbOneV <= kProbOneChunks * kProbChunk, "records fit LDS");
 
+// 0: the one-kernel form needs none.
 size_t probs_workspace_bytes(int B, int V) {
+  if (V <= kProbOneV) return 0;
   const size_t nch = (size_t)((V + kProbChunk - 1) / kProbChunk);
-  return (size_t)B * nch * sizeof(ProbRec);
+  return (size_t)B * (sizeof(ProbPlan) + nch * sizeof(double));
 }
 
 hipError_t launch_verify_probs(bool bf16, const void* tgt, long long tsb, long long tsk,
@@ -372,7 +454,8 @@ hipError_t launch_verify_probs(bool bf16, const void* tgt, long long tsb, long l
   a.V = V;
   a.nch = (V + kProbChunk - 1) / kProbChunk;
   a.eos_id = eos_id;
-  a.recs = static_cast<ProbRec*>(workspace);
+  a.plans = static_cast<ProbPlan*>(workspace);
+  a.recs = reinterpret_cast<double*>(a.plans + B);
   a.out_tokens = out_tokens;
   a.n_emitted = n_emitted;
   a.alpha_out = alpha_out;

@@ -155,16 +155,17 @@ def test_accept_ties_are_exact():
     assert got["path"][0] == O.PATH_BONUS and got["out_tokens"][0, 0] == 0
 
 
-def test_empty_residual_redraws_from_p():
+@pytest.mark.parametrize("V", [2000, 50000, 200000])
+def test_empty_residual_redraws_from_p(V):
     # p below q everywhere (the rows sum to less than one): nothing to correct with
-    V = 2000
     p = torch.full((3, 2, V), 2.0 ** -12)
     q = torch.full((3, 1, V), 2.0 ** -11)
     w = dict(target_probs=p, draft_probs=q, draft_tokens=torch.full((3, 1), 7, dtype=torch.int32),
              draft_len=torch.ones(3, dtype=torch.int32), u=torch.full((3, 1), 0.9),
              u_final=torch.tensor([0.0, 0.5, 0.99]))
     got = to_numpy(S.verify_probs(**on_gpu(w), debug=True))
-    assert got["out_tokens"][:, 0].tolist() == [0, 1000, 1980]
+    # every sum is exact but the last draw's t: the token is that of u_final
+    assert got["out_tokens"][:, 0].tolist() == [0, V // 2, int(np.float32(0.99) * float(V))]
     assert np.all(got["path"] == O.PATH_REJECT) and np.all(got["residual_mass"] == 0)
 
 
@@ -283,6 +284,7 @@ def test_streams_graphs_and_repeats(V):
 
 
 def test_python_refusals():
+    big = on_gpu(make(2, 2, 70000, F32, 30))
     w = on_gpu(make(2, 2, 100, F32, 30))
     with pytest.raises(TypeError):
         S.verify_probs(**dict(w, target_probs=w["target_probs"].half()))
@@ -295,7 +297,7 @@ def test_python_refusals():
     with pytest.raises(S.SpecVerifyError):
         S.verify_probs(**w, eos_id=100)
     with pytest.raises(S.SpecVerifyError) as e:
-        S.verify_probs(**w, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
+        S.verify_probs(**big, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
     assert e.value.status == 2
     empty = torch.empty(0, 3, 100, device=DEV)
     with pytest.raises(S.SpecVerifyError):

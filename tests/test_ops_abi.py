@@ -142,15 +142,15 @@ def test_verify_fp8_lm_head_workspace(lib):
 
 
 PROBS = ("t tsb tsk d dsb dsk dt tok n u uf B K V eos out ne ws wsb stream ap rm sp pa").split()
-PROBS_OK = dict(t=FAR[0], tsb=4000, tsk=1000, d=FAR[1], dsb=3000, dsk=1000, dt=0, tok=FAR[2],
-                n=FAR[3], u=FAR[4], uf=FAR[5], B=2, K=3, V=1000, eos=-1, out=FAR[6], ne=FAR[7],
+PROBS_OK = dict(t=FAR[0], tsb=360000, tsk=90000, d=FAR[1], dsb=270000, dsk=90000, dt=0, tok=FAR[2],
+                n=FAR[3], u=FAR[4], uf=FAR[5], B=2, K=3, V=90000, eos=-1, out=FAR[6], ne=FAR[7],
                 ws=FAR[8], wsb=1 << 20, stream=None, ap=None, rm=None, sp=None, pa=None)
 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(B=0), EINVAL), (dict(K=65), EINVAL), (dict(K=-1), EINVAL), (dict(V=0), EINVAL),
     (dict(V=4194305), EUNSUPPORTED), (dict(B=0x7fffffff, V=4096), EUNSUPPORTED),
-    (dict(dt=3), EINVAL), (dict(eos=1000), EINVAL), (dict(eos=-2), EINVAL), (dict(tsb=-1), EINVAL),
+    (dict(dt=3), EINVAL), (dict(eos=90000), EINVAL), (dict(eos=-2), EINVAL), (dict(tsb=-1), EINVAL),
     (dict(dsk=-1), EINVAL), (dict(tsb=1 << 62), EINVAL), (dict(t=None), EINVAL),
     (dict(tok=None), EINVAL), (dict(n=None), EINVAL), (dict(u=None), EINVAL), (dict(uf=None), EINVAL),
     (dict(out=None), EINVAL), (dict(ne=None), EINVAL), (dict(t=FAR[0] + 2), EINVAL),
@@ -163,7 +163,8 @@ def test_verify_probs_refuses(lib, kw, want):
 
 def test_verify_probs_workspace(lib):
     n = lib.specv_verify_probs_workspace_bytes
-    assert n(64, 4, 128256) == 64 * 126 * 16 and n(1, 0, 1) > 0 and n(1, 64, 4194304) > 0
+    assert n(64, 4, 128256) == 64 * (126 * 8 + 16) and n(1, 64, 4194304) > 0
+    assert n(1, 0, 1) == 0                                        # one kernel: none needed
     assert n(0, 4, 100) == 0 and n(1, 65, 100) == 0 and n(1, 1, 4194305) == 0
 
 
