@@ -188,9 +188,31 @@ constexpr bool kFp8Exact = sizeof(O) == 4;
 
 __device__ __forceinline__ void f8_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void f8_put(bf16_t* p, float v) { *p = (bf16_t)bf16_bits(v); }
+// Four consecutive logits, registers r .. r + 3 of an accumulator.
+__device__ __forceinline__ void f8_put4(float* p, const fp8_f32x16& c, int r) {
+  *reinterpret_cast<float4*>(p) = make_float4(c[r], c[r + 1], c[r + 2], c[r + 3]);
+}
+__device__ __forceinline__ void f8_put4(bf16_t* p, const fp8_f32x16& c, int r) {
+  uint2 w;
+  w.x = bf16_bits(c[r]) | bf16_bits(c[r + 1]) << 16;
+  w.y = bf16_bits(c[r + 2]) | bf16_bits(c[r + 3]) << 16;
+  *reinterpret_cast<uint2*>(p) = w;
+}
 
 __device__ __forceinline__ uint4 load16(const uint8_t* p) {
   return *reinterpret_cast<const uint4*>(p);
+}
+
+// 16 bytes of a weight, past the caches where the call reads it only once.
+template <bool ONCE>
+__device__ __forceinline__ uint4 load16_weight(const uint8_t* p) {
+  if constexpr (!ONCE) {
+    return load16(p);
+  } else {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
+  }
 }
 
 // Bytes 4 g .. 4 g + 3 of a row of nkb scale bytes as a word, 127 past the
@@ -215,75 +237,55 @@ __device__ __forceinline__ uint32_t fp8_scale_word(const Fp8ScaleBytes& s, int g
 }
 
 // Few hidden rows: the weights are read straight into registers, once, and
-// the kernel is bound by them.  A workgroup owns 32 vocabulary rows and up to
-// 32 MT hidden rows; its four waves split the runs (groups of four, one scale
-// word) and add their sums through LDS in a fixed order.
-template <int MT, typename O>
+// the kernel is bound by them (76 us for the 529 MB of 1 x 128256 x 4096, 6.9
+// TB/s).  A workgroup owns 32 vocabulary rows and up to 32 hidden rows; its
+// four waves split the runs (every fourth one each, so that together they read
+// 16 KB in a row) and add their sums through LDS in a fixed order.
+template <bool ONCE, typename O>
 __global__ __launch_bounds__(kF8Threads) void fp8_skinny_kernel(
     const uint8_t* __restrict__ H, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ P,
-    const uint32_t* __restrict__ ws, int M, int D, int V, int ngroup, O* __restrict__ out) {
-  __shared__ float red[kF8Waves][MT * 32][33];
+    const uint8_t* __restrict__ ws, int M, int D, int V, int ngroup, O* __restrict__ out) {
+  __shared__ float red[kF8Waves][32][33];
   const int group = blockIdx.x % ngroup;
-  const int m0 = (blockIdx.x / ngroup) * (32 * MT);
+  const int m0 = (blockIdx.x / ngroup) * 32;
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int h = lane / 32, l32 = lane % 32;
   const int nkb = D / kFp8Block, nk4 = (nkb + 3) / 4;
   const uint8_t* wrow = P + (size_t)group * nkb * kF8RunBytes + lane * 16;
-  const uint32_t* wsc = ws + (size_t)group * nk4 * kF8Group + l32;
-  const uint8_t* hrow[MT];
-  const uint8_t* hsc[MT];
+  const uint8_t* wsc = ws + (size_t)group * nk4 * (kF8Group * 4) + l32 * 4;
+  const size_t hm = (size_t)min(m0 + l32, M - 1);            // rows past M repeat the last
+  const uint8_t* hrow = H + hm * D + 32 * h;
+  const uint8_t* hsc = hs + hm * nkb;
+  fp8_f32x16 acc;
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const size_t m = (size_t)min(m0 + 32 * t + l32, M - 1);   // rows past M repeat the last
-    hrow[t] = H + m * D + 32 * h;
-    hsc[t] = hs + m * nkb;
-  }
-  fp8_f32x16 acc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[t][r] = 0.f;
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
 
-  auto run = [&](auto idx, int kb, uint32_t sa, const uint32_t* sb) {
-    constexpr int I = decltype(idx)::value;
+#pragma unroll 4
+  for (int kb = wave; kb < nkb; kb += kF8Waves) {
     uint4 a[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) a[s] = load16(wrow + (size_t)kb * kF8RunBytes + s * 1024);
+    for (int s = 0; s < 4; ++s)
+      a[s] = load16_weight<ONCE>(wrow + (size_t)kb * kF8RunBytes + s * 1024);
+    const uint32_t sa = wsc[(kb / 4) * (kF8Group * 4) + kb % 4];
+    uint4 b[4];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      uint4 b[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        b[s] = load16(hrow[t] + kb * kFp8Block + 64 * (s / 2) + 16 * (s % 2));
-      acc[t] = fp8_step<kFp8Exact<O>, I>({a[0], a[1]}, {b[0], b[1]}, acc[t], sa, sb[t]);
-      acc[t] = fp8_step<kFp8Exact<O>, I>({a[2], a[3]}, {b[2], b[3]}, acc[t], sa, sb[t]);
-    }
-  };
-  for (int g = wave; g < nk4; g += kF8Waves) {
-    const uint32_t sa = wsc[g * kF8Group];
-    const int left = nkb - 4 * g;
-    uint32_t sb[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) sb[t] = fp8_scale_word(fp8_scale_load(hsc[t], g, nkb), g, nkb);
-    run(std::integral_constant<int, 0>{}, 4 * g, sa, sb);
-    if (left > 1) run(std::integral_constant<int, 1>{}, 4 * g + 1, sa, sb);
-    if (left > 2) run(std::integral_constant<int, 2>{}, 4 * g + 2, sa, sb);
-    if (left > 3) run(std::integral_constant<int, 3>{}, 4 * g + 3, sa, sb);
+    for (int s = 0; s < 4; ++s)
+      b[s] = load16(hrow + kb * kFp8Block + 64 * (s / 2) + 16 * (s % 2));
+    const uint32_t sb = hsc[kb];
+    acc = fp8_step<kFp8Exact<O>, 0>({a[0], a[1]}, {b[0], b[1]}, acc, sa, sb);
+    acc = fp8_step<kFp8Exact<O>, 0>({a[2], a[3]}, {b[2], b[3]}, acc, sa, sb);
   }
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-      red[wave][32 * t + l32][8 * (r / 4) + r % 4 + 4 * h] = acc[t][r];
+  for (int r = 0; r < 16; ++r) red[wave][l32][8 * (r / 4) + r % 4 + 4 * h] = acc[r];
   __syncthreads();
-  for (int i = threadIdx.x; i < MT * 32 * 32; i += kF8Threads) {
+  for (int i = threadIdx.x; i < 32 * 32; i += kF8Threads) {
     const int m = i / 32, v = i % 32;
+    if (m0 + m >= M) break;                                  // m only grows
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kF8Waves; ++w) s += red[w][m][v];
-    if (m0 + m < M && group * kF8Group + v < V)
-      f8_put(out + (size_t)(m0 + m) * V + group * kF8Group + v, s);
+    if (group * kF8Group + v < V) f8_put(out + (size_t)(m0 + m) * V + group * kF8Group + v, s);
   }
 }
 
@@ -313,20 +315,22 @@ __device__ __forceinline__ void lds_barrier() {
 constexpr int kTileVocab = 256;
 constexpr int kTileGroups = kTileVocab / kF8Group;
 constexpr int kXcds = 8;
-constexpr int kPin = 4;
 static_assert(kTileGroups == 2 * kF8Waves, "two packed groups to a wave");
 
-template <int MT, typename O>
+template <int MT, int RING, bool ONCE, typename O>
 __global__ __launch_bounds__(kF8Threads, 2) void fp8_tile_kernel(
     const uint8_t* __restrict__ H, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ P,
     const uint32_t* __restrict__ ws, int M, int D, int V, int ngroup, int nrb, int nwork,
     O* __restrict__ out) {
   constexpr int kRows = MT * 32;
   constexpr int kBuf = kRows * kFp8Block;
-  constexpr int kTrStride = kTileVocab + 8;                 // epilogue rows, bfloat16
   static_assert(kRows <= kF8Threads, "one row's scales to a thread");
-  static_assert(2 * kBuf >= 32 * kTrStride * (int)sizeof(bf16_t), "the epilogue reuses the buffers");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuf];
+  // epilogue: 32 rows of bfloat16 or 16 of float32 at a time, in the run buffers
+  constexpr int kTrStride = kTileVocab + 16 / (int)sizeof(O);
+  constexpr int kTrRows = 64 / (int)sizeof(O);
+  constexpr int kTrBytes = kTrRows * kTrStride * (int)sizeof(O);
+  static_assert(4 % RING == 0, "the weight ring indexes statically over a group of runs");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuf > kTrBytes ? 2 * kBuf : kTrBytes];
   __shared__ uint32_t lsc[2][kF8Threads];                    // words past kRows are not read
 
   const int per = (nwork + kXcds - 1) / kXcds;
@@ -365,58 +369,62 @@ __global__ __launch_bounds__(kF8Threads, 2) void fp8_tile_kernel(
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[a][t][r] = 0.f;
 
-  uint4 wr[2][2][4], st[MT];
-  auto load_w = [&](int kb, uint4 (&d)[2][4]) {             // past the end: the last run again
-    const size_t at = (size_t)min(kb, nkb - 1) * kF8RunBytes;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      d[0][s] = load16(w0 + at + lane16 + s * 1024);
-      d[1][s] = load16(w1 + at + lane16 + s * 1024);
+  uint4 wr[RING][2][4], st[MT];
+  // load i of the MT + 8 of a run: staged hidden rows of run kb, then weights of
+  // run kbw (past the end: the last run again)
+  auto load = [&](int i, int kb, int kbw, uint4 (&d)[2][4]) {
+    if (i < MT) {
+      st[i] = load16(hb + (size_t)min(kb, nkb - 1) * kFp8Block + hoff[i]);
+    } else {
+      const int a = (i - MT) / 4, s = (i - MT) % 4;
+      d[a][s] = load16_weight<ONCE>((a ? w1 : w0) + (size_t)min(kbw, nkb - 1) * kF8RunBytes +
+                                    s * 1024 + lane16);
     }
   };
-  auto load_h = [&](int kb) {
-    const uint8_t* src = hb + (size_t)min(kb, nkb - 1) * kFp8Block;
-#pragma unroll
-    for (int j = 0; j < MT; ++j) st[j] = load16(src + hoff[j]);
-  };
-  auto store_h = [&](int kb, int b) {                       // zeros past the end
-    const uint32_t keep = kb < nkb ? 0xffffffffu : 0u;
+  auto store_h = [&](int b) {
 #pragma unroll
     for (int j = 0; j < MT; ++j)
-      *reinterpret_cast<uint4*>(lds + b * kBuf + slot + j * 32 * kFp8Block) =
-          make_uint4(st[j].x & keep, st[j].y & keep, st[j].z & keep, st[j].w & keep);
+      *reinterpret_cast<uint4*>(lds + b * kBuf + slot + j * 32 * kFp8Block) = st[j];
   };
 
   uint32_t sa0 = s0[l32], sa1 = s1[l32], sb[MT];
-  load_h(0);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) load(i, 0, 0, wr[0]);
   lsc[0][tid] = fp8_scale_word(fp8_scale_load(hsrow, 0, nkb), 0, nkb);
-  load_w(0, wr[0]);
-  store_h(0, 0);
+#pragma unroll
+  for (int r = 0; r < RING - 1; ++r)
+#pragma unroll
+    for (int i = MT; i < MT + 8; ++i) load(i, 0, r, wr[r]);
+  store_h(0);
   lds_barrier();
 
   auto run = [&](auto idx, int kb) {
     constexpr int I = decltype(idx)::value;
-    load_h(kb + 1);
-    load_w(kb + 1, wr[(I + 1) % 2]);
-    __builtin_amdgcn_sched_barrier(0);
     const uint8_t* buf = lds + (I % 2) * kBuf + l32 * kFp8Block;
-    const uint4(&w)[2][4] = wr[I % 2];
+    const uint4(&w)[2][4] = wr[I % RING];
     const int sw = (l32 >> 1) & 7;
+    constexpr int kPin = MT;                               // products kept together
+    constexpr int kParts = 2 * MT / kPin;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int i = 0; i < 2 * MT; ++i) {
+      const int s = i / MT, t = i % MT;
+      if (i % kPin == 0) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const Fp8Bytes b = {load16(buf + t * 32 * kFp8Block + (((4 * s + 2 * h) ^ sw) * 16)),
-                            load16(buf + t * 32 * kFp8Block + (((4 * s + 2 * h + 1) ^ sw) * 16))};
-        acc[0][t] = fp8_step<kFp8Exact<O>, I>({w[0][2 * s], w[0][2 * s + 1]}, b, acc[0][t], sa0, sb[t]);
-        acc[1][t] = fp8_step<kFp8Exact<O>, I>({w[1][2 * s], w[1][2 * s + 1]}, b, acc[1][t], sa1, sb[t]);
-        if ((s * MT + t) % kPin == kPin - 1) __builtin_amdgcn_sched_barrier(0);
+        for (int l = (i / kPin) * (MT + 8) / kParts; l < (i / kPin + 1) * (MT + 8) / kParts; ++l)
+          load(l, kb + 1, kb + RING - 1, wr[(I + RING - 1) % RING]);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      const Fp8Bytes b = {load16(buf + t * 32 * kFp8Block + (((4 * s + 2 * h) ^ sw) * 16)),
+                          load16(buf + t * 32 * kFp8Block + (((4 * s + 2 * h + 1) ^ sw) * 16))};
+      acc[0][t] = fp8_step<kFp8Exact<O>, I>({w[0][2 * s], w[0][2 * s + 1]}, b, acc[0][t], sa0, sb[t]);
+      acc[1][t] = fp8_step<kFp8Exact<O>, I>({w[1][2 * s], w[1][2 * s + 1]}, b, acc[1][t], sa1, sb[t]);
+      if (i % kPin == kPin - 1) __builtin_amdgcn_sched_barrier(0);
+    }
     __builtin_amdgcn_sched_barrier(0);
-    store_h(kb + 1, (I + 1) % 2);
+    store_h((I + 1) % 2);
   };
-  // groups of four runs, one scale word; runs past the last multiply zeros
-  for (int g = 0; g < nk4; ++g) {
+  // groups of four runs, one scale word
+  for (int g = 0;; ++g) {
     const int next = min(g + 1, nk4 - 1);
     const uint32_t n0 = s0[next * kF8Group + l32], n1 = s1[next * kF8Group + l32];
     const Fp8ScaleBytes nh = fp8_scale_load(hsrow, next, nkb);
@@ -424,114 +432,173 @@ __global__ __launch_bounds__(kF8Threads, 2) void fp8_tile_kernel(
     for (int t = 0; t < MT; ++t) sb[t] = lsc[g & 1][t * 32 + l32];
     run(std::integral_constant<int, 0>{}, 4 * g);
     lds_barrier();
+    if (4 * g + 1 == nkb) break;
     run(std::integral_constant<int, 1>{}, 4 * g + 1);
     lds_barrier();
+    if (4 * g + 2 == nkb) break;
     run(std::integral_constant<int, 2>{}, 4 * g + 2);
     lds_barrier();
+    if (4 * g + 3 == nkb) break;
     run(std::integral_constant<int, 3>{}, 4 * g + 3);
     lsc[(g + 1) & 1][tid] = fp8_scale_word(nh, next, nkb);
     lds_barrier();
+    if (4 * g + 4 == nkb) break;
     sa0 = n0;
     sa1 = n1;
   }
 
   // acc[a][t][r] is the logit of row 32 t + l32 of the block and vocabulary id
   // 64 wave + 32 a + 8 (r / 4) + r % 4 + 4 h of the tile.
+  // They leave through LDS, so that a wave's stores cover consecutive ids: 16
+  // bytes a lane where every row starts 16-byte aligned, else two bfloat16
+  // logits that share an aligned word, or one float32 logit (stored straight
+  // from the accumulators an odd V cost 31 instead of 17 us at 320 x 20001 x
+  // 1152).
   const int vb = wave * 64 + 4 * h;
-  const int v0 = tile * kTileVocab;
-  const bool whole = V % (16 / sizeof(O)) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-  if constexpr (sizeof(O) == 2) {
-    if (whole) {
-      // 32 rows at a time through LDS, so that the stores cover whole 512-byte
-      // row segments
-      bf16_t* tr = reinterpret_cast<bf16_t*>(lds);
+  const int v0 = tile * kTileVocab, nv = min(kTileVocab, V - v0);
+  constexpr int kVec = 16 / sizeof(O);
+  const bool whole = V % kVec == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+  O* tr = reinterpret_cast<O*>(lds);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int part = 0; part < 32 / kTrRows; ++part) {
+      const int r0 = t * 32 + part * kTrRows;               // first row of the part in the block
+      if (32 == kTrRows || l32 / kTrRows == part) {
+        O* row = tr + (l32 % kTrRows) * kTrStride + vb;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint2 w;
-            w.x = bf16_bits(acc[a][t][4 * q]) | bf16_bits(acc[a][t][4 * q + 1]) << 16;
-            w.y = bf16_bits(acc[a][t][4 * q + 2]) | bf16_bits(acc[a][t][4 * q + 3]) << 16;
-            *reinterpret_cast<uint2*>(tr + l32 * kTrStride + vb + 32 * a + 8 * q) = w;
-          }
-        lds_barrier();
+          for (int q = 0; q < 4; ++q) f8_put4(row + 32 * a + 8 * q, acc[a][t], 4 * q);
+      }
+      lds_barrier();
+      if (whole) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int p = tid + i * kF8Threads, row = p / 32, c = (p % 32) * 8;
-          if (m0 + t * 32 + row < M && v0 + c < V)
-            *reinterpret_cast<uint4*>(out + (size_t)(m0 + t * 32 + row) * V + v0 + c) =
+        for (int i = 0; i < kTrRows * kTileVocab / kVec / kF8Threads; ++i) {
+          const int p = tid + i * kF8Threads, row = p / (kTileVocab / kVec);
+          const int c = p % (kTileVocab / kVec) * kVec;
+          if (m0 + r0 + row < M && c < nv)
+            *reinterpret_cast<uint4*>(out + (size_t)(m0 + r0 + row) * V + v0 + c) =
                 *reinterpret_cast<const uint4*>(tr + row * kTrStride + c);
         }
-        lds_barrier();
-      }
-      return;
-    }
-  }
+      } else {
+        constexpr int kLog = 4 / sizeof(O);                  // logits of a 4-byte store
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = m0 + t * 32 + l32;
-    if (m >= M) continue;
-    O* row = out + (size_t)m * V;
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int v = v0 + vb + 32 * a + 8 * q;
-        if constexpr (sizeof(O) == 4) {
-          if (whole && v < V) {                             // V a multiple of 4: v + 3 < V too
-            *reinterpret_cast<float4*>(row + v) =
-                make_float4(acc[a][t][4 * q], acc[a][t][4 * q + 1], acc[a][t][4 * q + 2],
-                            acc[a][t][4 * q + 3]);
-            continue;
+        for (int i = 0; i < kTrRows * kTileVocab / kLog / kF8Threads; ++i) {
+          const int p = tid + i * kF8Threads, row = p / (kTileVocab / kLog);
+          if (m0 + r0 + row >= M) continue;
+          O* dst = out + (size_t)(m0 + r0 + row) * V + v0;
+          const O* src = tr + row * kTrStride;
+          if constexpr (sizeof(O) == 4) {
+            const int c = p % kTileVocab;
+            if (c < nv) dst[c] = src[c];
+          } else {
+            // aligned words start at the row's first logit or its second; a
+            // first or last logit without a partner is stored alone
+            const int odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
+            const int c = odd + 2 * (p % (kTileVocab / 2));
+            if (odd && c == 1) dst[0] = src[0];
+            if (c + 1 < nv)
+              *reinterpret_cast<uint32_t*>(dst + c) = (uint32_t)src[c] | (uint32_t)src[c + 1] << 16;
+            else if (c < nv)
+              dst[c] = src[c];
           }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (v + i < V) f8_put(row + v + i, acc[a][t][4 * q + i]);
       }
-  }
+      lds_barrier();
+    }
 }
 
-template <int MT, typename O>
-hipError_t fp8_tiles(const uint8_t* H, const uint8_t* hs, const uint8_t* P, const uint32_t* ws,
-                     int M, int D, int V, O* out, hipStream_t stream) {
-  const int nrb = (M + 32 * MT - 1) / (32 * MT);
-  const size_t nwork = (size_t)((V + kTileVocab - 1) / kTileVocab) * nrb;
+struct Fp8Args {
+  const uint8_t *H, *hs, *P, *ws;
+  int M, D, V;
+  hipStream_t stream;
+};
+
+template <int MT, int RING, bool ONCE, typename O>
+hipError_t fp8_tiles(const Fp8Args& a, O* out) {
+  const int nrb = (a.M + 32 * MT - 1) / (32 * MT);
+  const size_t nwork = (size_t)((a.V + kTileVocab - 1) / kTileVocab) * nrb;
   const size_t blocks = (nwork + kXcds - 1) / kXcds * kXcds;
   if (blocks > 0x7fffffffu) return hipErrorInvalidConfiguration;
-  fp8_tile_kernel<MT, O><<<dim3((unsigned)blocks), dim3(kF8Threads), 0, stream>>>(
-      H, hs, P, ws, M, D, V, fp8_groups(V), nrb, (int)nwork, out);
+  fp8_tile_kernel<MT, RING, ONCE, O><<<dim3((unsigned)blocks), dim3(kF8Threads), 0, a.stream>>>(
+      a.H, a.hs, a.P, reinterpret_cast<const uint32_t*>(a.ws), a.M, a.D, a.V, fp8_groups(a.V), nrb,
+      (int)nwork, out);
   return hipGetLastError();
 }
 
-template <typename O>
-hipError_t fp8_head(const uint8_t* H, const uint8_t* hs, const uint8_t* P, int M, int D, int V,
-                    O* out, hipStream_t stream) {
-  const uint32_t* ws = reinterpret_cast<const uint32_t*>(P + fp8_packed_scale_off(V, D));
-  const int ng = fp8_groups(V);
-  if (M > 64) {
-    // row blocks of 96 where they leave fewer rows empty, else of 128 (669 vs
-    // 714 us at 1152 x 152064 x 4096).  Float32 logits always take 96: the
-    // wider operands would spill at 128.
-    if constexpr (!kFp8Exact<O>)
-      if ((M + 127) / 128 * 128 <= (M + 95) / 96 * 96)
-        return fp8_tiles<4, O>(H, hs, P, ws, M, D, V, out, stream);
-    return fp8_tiles<3, O>(H, hs, P, ws, M, D, V, out, stream);
-  }
-  const dim3 grid((unsigned)ng), thr(kF8Threads);
-  if (M <= 32) fp8_skinny_kernel<1, O><<<grid, thr, 0, stream>>>(H, hs, P, ws, M, D, V, ng, out);
-  else fp8_skinny_kernel<2, O><<<grid, thr, 0, stream>>>(H, hs, P, ws, M, D, V, ng, out);
+template <bool ONCE, typename O>
+hipError_t fp8_skinny(const Fp8Args& a, O* out) {
+  const int ng = fp8_groups(a.V);
+  const size_t blocks = (size_t)ng * ((a.M + 31) / 32);
+  if (blocks > 0x7fffffffu) return hipErrorInvalidConfiguration;
+  fp8_skinny_kernel<ONCE, O><<<dim3((unsigned)blocks), dim3(kF8Threads), 0, a.stream>>>(
+      a.H, a.hs, a.P, a.ws, a.M, a.D, a.V, ng, out);
   return hipGetLastError();
+}
+
+constexpr double kFp8CacheBytes = 256.0 * (1 << 20);
+
+// Which product: 0 the skinny one, MT = 1..4 tiles of 32 MT hidden rows, by an
+// estimate of each one's time in nanoseconds, fitted to bfloat16 logits from
+// 1 x 128256 x 4096 to 1152 x 152064 x 4096 and down to 32 x 4000 x 512.
+//  - The skinny product reads the weights once for every 32 rows: 5.6 TB/s (4.3
+//    from memory with more than 16 rows, where the hidden rows' reads tell),
+//    6.5 for the blocks after the first.
+//  - A tile takes 0.65 to 1.06 us a run, two on a CU as long as one after the
+//    other; a little more than one to a CU on average is two on some.  All of
+//    them take at least the weights' time, 34 GB/s to a busy CU and 5.4 TB/s,
+//    4.3 where more than one row block reads them.
+int fp8_choice(int M, int D, int V, bool exact) {
+  const double bytes = (double)V * D, runs = D / kFp8Block;
+  const double tiles = (V + kTileVocab - 1) / kTileVocab;
+  const double first = M > 16 && bytes > kFp8CacheBytes ? 4300 : 5600;
+  double best = 3500 + bytes / first + ((M + 31) / 32 - 1) * bytes / 6500;
+  int choice = 0;
+  const double run_ns[5] = {0, 650, 730, 870, 1060};
+  for (int mt = 1; mt <= (exact ? 3 : 4); ++mt) {
+    const int nrb = (M + 32 * mt - 1) / (32 * mt);
+    const double cus = tiles * nrb / 256;
+    const double load = cus <= 1 ? 1 : cus <= 1.55 ? 1.55 : cus < 3 ? 1.12 * cus : cus;
+    const double work = load * runs * run_ns[mt] * (exact ? 1.6 : 1);
+    double rate = nrb == 1 ? 5400 : 4300;
+    if (rate > 34 * tiles * nrb) rate = 34 * tiles * nrb;
+    const double t = 3000 + (work > bytes / rate ? work : bytes / rate);
+    if (t < best) {
+      best = t;
+      choice = mt;
+    }
+  }
+  return choice;
+}
+
+// Weights larger than the memory-side cache (256 MB) and read once go past
+// the caches: 88 -> 76 us at 1 x 128256 x 4096, 117 -> 101 us at 128 rows.
+// Smaller ones may still be there from the last call (20 instead of 22 us at
+// 6 x 32000 x 4096), and with several row blocks all but the first find them
+// in L2 (218 instead of 256 us at 320 rows).
+template <bool ONCE, typename O>
+hipError_t fp8_run(const Fp8Args& a, int choice, O* out) {
+  if (choice == 0) return fp8_skinny<ONCE>(a, out);
+  if (choice == 1) return fp8_tiles<1, 4, ONCE>(a, out);
+  if (choice == 2) return fp8_tiles<2, 4, ONCE>(a, out);
+  if constexpr (!kFp8Exact<O>)                               // float32: 4 would spill
+    if (choice == 4) return fp8_tiles<4, 2, ONCE>(a, out);
+  return fp8_tiles<3, 2, ONCE>(a, out);
+}
+template <typename O>
+hipError_t fp8_head(const Fp8Args& a, O* out) {
+  const int choice = fp8_choice(a.M, a.D, a.V, kFp8Exact<O>);
+  const int rows = choice == 0 ? 32 : 32 * choice;
+  return a.M <= rows && (double)a.V * a.D > kFp8CacheBytes ? fp8_run<true>(a, choice, out)
+                                                              : fp8_run<false>(a, choice, out);
 }
 
 hipError_t launch_fp8_head(const uint8_t* hidden, const uint8_t* hscale, const void* packed, int M,
                            int D, int V, void* logits, bool bf16, hipStream_t stream) {
   const uint8_t* P = static_cast<const uint8_t*>(packed);
-  if (bf16)
-    return fp8_head(hidden, hscale, P, M, D, V, static_cast<bf16_t*>(logits), stream);
-  return fp8_head(hidden, hscale, P, M, D, V, static_cast<float*>(logits), stream);
+  const Fp8Args a = {hidden, hscale, P, P + fp8_packed_scale_off(V, D), M, D, V, stream};
+  return bf16 ? fp8_head(a, static_cast<bf16_t*>(logits)) : fp8_head(a, static_cast<float*>(logits));
 }
 
 // Largest grid of any product (workgroups), for the host's size check.

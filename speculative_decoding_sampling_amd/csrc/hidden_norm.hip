@@ -5,7 +5,7 @@
 //
 // Every row is read once, kept in registers through both reductions and
 // written once (r' and y), so the bytes moved are the floor; a workgroup owns
-// a row, each thread 8 values at a time (16-byte loads of bfloat16), as many
+// a row, each thread 8 values at a time, as many
 // threads as the row has such groups, up to 1024.  The sums of squares are
 // float32: per thread in order, then the wave on DPP moves, then the waves
 // through LDS in a fixed order.
@@ -33,10 +33,17 @@ struct NormArgs {
   float scale, eps;
 };
 
-// Values e0 .. e0 + 7 of a row as floats; those at or past D read as 0.
-template <typename T, bool VEC>
-__device__ __forceinline__ void norm_load(const T* row, int e0, int D, float* v) {
-  if constexpr (VEC) {
+// How a thread's 8 values of a group lie in the row: 8 neighbours in 16-byte
+// loads; 8 neighbours one at a time (8-bit output of arrays off 16 bytes, whose
+// runs of 128 are 16 threads'); or a workgroup's width apart, one at a time, so
+// that neighbouring threads read neighbouring values (rows of any length: 8.8
+// -> 4.2 us at 37 x 2047 float32 against 8 neighbours).
+enum NormLayout { kWide, kNeighbours, kApart };
+
+// Values e0, e0 + es, .. of a row as floats; those at or past D read as 0.
+template <typename T, int LAYOUT>
+__device__ __forceinline__ void norm_load(const T* row, int e0, int es, int D, float* v) {
+  if constexpr (LAYOUT == kWide) {
     if (e0 < D) {                                        // D is a multiple of 8
 #pragma unroll
       for (int i = 0; i < 8; i += Elem<T>::kPerVec) load_vec_fast(row, e0 + i, v + i);
@@ -46,24 +53,24 @@ __device__ __forceinline__ void norm_load(const T* row, int e0, int D, float* v)
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = e0 + i < D ? to_f32(row[e0 + i]) : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = e0 + i * es < D ? to_f32(row[e0 + i * es]) : 0.f;
   }
 }
 
 // The same for a weight row of either type (uniform over the grid).
-template <bool VEC>
-__device__ __forceinline__ void norm_load_w(const void* w, bool w_bf16, size_t off, int e0, int D,
-                                            float* v) {
-  if (w_bf16) norm_load<bf16_t, VEC>(static_cast<const bf16_t*>(w) + off, e0, D, v);
-  else norm_load<float, VEC>(static_cast<const float*>(w) + off, e0, D, v);
+template <int LAYOUT>
+__device__ __forceinline__ void norm_load_w(const void* w, bool w_bf16, size_t off, int e0, int es,
+                                            int D, float* v) {
+  if (w_bf16) norm_load<bf16_t, LAYOUT>(static_cast<const bf16_t*>(w) + off, e0, es, D, v);
+  else norm_load<float, LAYOUT>(static_cast<const float*>(w) + off, e0, es, D, v);
 }
 
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(bf16_t* p, float v) { *p = (bf16_t)bf16_bits(v); }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void norm_store(T* row, int e0, int D, const float* v) {
-  if constexpr (VEC) {
+template <typename T, int LAYOUT>
+__device__ __forceinline__ void norm_store(T* row, int e0, int es, int D, const float* v) {
+  if constexpr (LAYOUT == kWide) {
     if (e0 >= D) return;
     if constexpr (sizeof(T) == 4) {
       *reinterpret_cast<float4*>(row + e0) = make_float4(v[0], v[1], v[2], v[3]);
@@ -79,7 +86,7 @@ __device__ __forceinline__ void norm_store(T* row, int e0, int D, const float* v
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (e0 + i < D) put(row + e0 + i, v[i]);
+      if (e0 + i * es < D) put(row + e0 + i * es, v[i]);
   }
 }
 
@@ -99,7 +106,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // Rows of more than 2 groups per thread leave the residual in memory until
 // the first reduction is done: with both rows in registers 1024 threads
 // would spill.
-template <typename X, typename R, int OUT, int NV, bool VEC>
+template <typename X, typename R, int OUT, int NV, int LAYOUT>
 __global__ __launch_bounds__(kNormMaxThreads) void hidden_norm_kernel(NormArgs a) {
   constexpr bool kEarly = NV <= 2;
   __shared__ float red[2][kNormMaxThreads / kWave];
@@ -109,12 +116,19 @@ __global__ __launch_bounds__(kNormMaxThreads) void hidden_norm_kernel(NormArgs a
   const R* r = static_cast<const R*>(a.r) + off;
   const size_t goff = (size_t)(m / a.rows_per_gate) * D;
 
+  // group j's first value and the distance to the next
+  const int es = LAYOUT == kApart ? (int)blockDim.x : 1;
+  auto at = [&](int j) {
+    return LAYOUT == kApart ? (int)(j * 8 * blockDim.x + threadIdx.x)
+                            : (int)(threadIdx.x + j * blockDim.x) * 8;
+  };
+
   float h[NV][8], res[kEarly ? NV : 1][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e0 = (threadIdx.x + j * blockDim.x) * 8;
-    norm_load<X, VEC>(x, e0, D, h[j]);
-    if constexpr (kEarly) norm_load<R, VEC>(r, e0, D, res[j]);
+    const int e0 = at(j);
+    norm_load<X, LAYOUT>(x, e0, es, D, h[j]);
+    if constexpr (kEarly) norm_load<R, LAYOUT>(r, e0, es, D, res[j]);
   }
   float f = a.scale;
   if (a.w1) {
@@ -128,33 +142,33 @@ __global__ __launch_bounds__(kNormMaxThreads) void hidden_norm_kernel(NormArgs a
   float ss = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e0 = (threadIdx.x + j * blockDim.x) * 8;
+    const int e0 = at(j);
     float c[8];
     if (a.w1) {
-      norm_load_w<VEC>(a.w1, a.w_bf16, 0, e0, D, c);
+      norm_load_w<LAYOUT>(a.w1, a.w_bf16, 0, e0, es, D, c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[j][i] *= c[i];
     }
     if (a.gate) {
-      norm_load_w<VEC>(a.gate, a.w_bf16, goff, e0, D, c);
+      norm_load_w<LAYOUT>(a.gate, a.w_bf16, goff, e0, es, D, c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[j][i] *= c[i];
     }
     float* rj = res[kEarly ? j : 0];
-    if constexpr (!kEarly) norm_load<R, VEC>(r, e0, D, rj);
+    if constexpr (!kEarly) norm_load<R, LAYOUT>(r, e0, es, D, rj);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       h[j][i] = fmaf(f, h[j][i], rj[i]);
       ss = fmaf(h[j][i], h[j][i], ss);
     }
-    norm_store<R, VEC>(static_cast<R*>(a.r_out) + off, e0, D, h[j]);
+    norm_store<R, LAYOUT>(static_cast<R*>(a.r_out) + off, e0, es, D, h[j]);
   }
   f = 1.f / sqrtf(block_sum(ss, red[1]) / (float)D + a.eps);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e0 = (threadIdx.x + j * blockDim.x) * 8;
+    const int e0 = at(j);
     float c[8];
-    norm_load_w<VEC>(a.w2, a.w_bf16, 0, e0, D, c);
+    norm_load_w<LAYOUT>(a.w2, a.w_bf16, 0, e0, es, D, c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] *= h[j][i] * f;
     if constexpr (OUT == SPECV_OUT_E4M3) {
@@ -167,17 +181,18 @@ __global__ __launch_bounds__(kNormMaxThreads) void hidden_norm_kernel(NormArgs a
         if (threadIdx.x % kFp8Lanes == 0) a.out_scale[(off + e0) / kFp8Block] = (uint8_t)byte;
       }
     } else if constexpr (OUT == SPECV_OUT_F32) {
-      norm_store<float, VEC>(static_cast<float*>(a.out) + off, e0, D, c);
+      norm_store<float, LAYOUT>(static_cast<float*>(a.out) + off, e0, es, D, c);
     } else {
-      norm_store<bf16_t, VEC>(static_cast<bf16_t*>(a.out) + off, e0, D, c);
+      norm_store<bf16_t, LAYOUT>(static_cast<bf16_t*>(a.out) + off, e0, es, D, c);
     }
   }
 }
 
 template <typename X, typename R, int OUT, int NV>
 void norm_launch(const NormArgs& a, int M, int threads, bool vec, hipStream_t stream) {
-  if (vec) hidden_norm_kernel<X, R, OUT, NV, true><<<dim3(M), dim3(threads), 0, stream>>>(a);
-  else hidden_norm_kernel<X, R, OUT, NV, false><<<dim3(M), dim3(threads), 0, stream>>>(a);
+  constexpr int kNarrow = OUT == SPECV_OUT_E4M3 ? kNeighbours : kApart;
+  if (vec) hidden_norm_kernel<X, R, OUT, NV, kWide><<<dim3(M), dim3(threads), 0, stream>>>(a);
+  else hidden_norm_kernel<X, R, OUT, NV, kNarrow><<<dim3(M), dim3(threads), 0, stream>>>(a);
 }
 
 template <typename X, typename R, int OUT>
