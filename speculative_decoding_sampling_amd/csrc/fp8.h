@@ -52,11 +52,14 @@ __device__ __forceinline__ uint2 fp8_pack8(const float* v, uint32_t& byte) {
   return r;
 }
 
-// float -> bfloat16 bits, round to nearest even; a NaN stays one.
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > kInfBits) return (u >> 16) | 0x40u;
-  return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+// Two floats as bfloat16 words, round to nearest even, a NaN stays one: one
+// instruction for both.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef float Float2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 Bf16x2 __attribute__((ext_vector_type(2)));
+  const Float2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, Bf16x2));
 }
+__device__ __forceinline__ bf16_t bf16_bits(float f) { return (bf16_t)bf16_pair(f, f); }
 
 }  // namespace specv

@@ -187,15 +187,15 @@ template <typename O>
 constexpr bool kFp8Exact = sizeof(O) == 4;
 
 __device__ __forceinline__ void f8_put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void f8_put(bf16_t* p, float v) { *p = (bf16_t)bf16_bits(v); }
+__device__ __forceinline__ void f8_put(bf16_t* p, float v) { *p = bf16_bits(v); }
 // Four consecutive logits, registers r .. r + 3 of an accumulator.
 __device__ __forceinline__ void f8_put4(float* p, const fp8_f32x16& c, int r) {
   *reinterpret_cast<float4*>(p) = make_float4(c[r], c[r + 1], c[r + 2], c[r + 3]);
 }
 __device__ __forceinline__ void f8_put4(bf16_t* p, const fp8_f32x16& c, int r) {
   uint2 w;
-  w.x = bf16_bits(c[r]) | bf16_bits(c[r + 1]) << 16;
-  w.y = bf16_bits(c[r + 2]) | bf16_bits(c[r + 3]) << 16;
+  w.x = bf16_pair(c[r], c[r + 1]);
+  w.y = bf16_pair(c[r + 2], c[r + 3]);
   *reinterpret_cast<uint2*>(p) = w;
 }
 

@@ -4,11 +4,20 @@
 //   r' = r + scale * g * N(x; w1),  y = N(r'; w2),  N(v; w) = w v / sqrt(mean(v^2) + eps)
 //
 // Every row is read once, kept in registers through both reductions and
-// written once (r' and y), so the bytes moved are the floor; a workgroup owns
-// a row, each thread 8 values at a time, as many
-// threads as the row has such groups, up to 1024.  The sums of squares are
-// float32: per thread in order, then the wave on DPP moves, then the waves
-// through LDS in a fixed order.
+// written once (r' and y), so the bytes moved are the floor.  A workgroup owns
+// a row, each thread 8 values, up to 1024 threads: a row's latency is two
+// reductions and is shortest with the fewest values a thread (5 x 4096 bfloat16:
+// 512 threads 4.2 us, 256 5.4, 128 8.1), and many rows keep two to four
+// workgroups on a compute unit.  The sums of squares are float32: per thread
+// in order, then the wave and the waves' sums on DPP moves, a fixed order.
+//
+// 2304 x 8192: 33.0 us from bfloat16 to 8-bit values (4.0 TB/s), 44.7 us with a
+// float32 residual (4.6 TB/s; a large copy reaches 4.9).  The narrow types are
+// bound by their instructions as much as by memory: packed conversions, one
+// reciprocal root and DPP sums took it from 37.9 us.  Workgroups that stay and
+// fetch the next row ahead gave 37.9 -> 35.8 us before that, but 46 -> 57 us with a float32
+// residual (registers), loads past the caches 33.0 -> 30.3 but 13.7 -> 14.9 us at
+// 1024 x 8192, where the rows still lie in them.
 //
 // y is formed from r' before r' is rounded to its own type: one rounding less
 // between the residual stream and the logits.
@@ -30,14 +39,14 @@ struct NormArgs {
   uint8_t* out_scale;
   int D, rows_per_gate;
   bool w_bf16;          // type of w1, gate and w2
-  float scale, eps;
+  float scale, eps, inv_d;
 };
 
 // How a thread's 8 values of a group lie in the row: 8 neighbours in 16-byte
 // loads; 8 neighbours one at a time (8-bit output of arrays off 16 bytes, whose
 // runs of 128 are 16 threads'); or a workgroup's width apart, one at a time, so
 // that neighbouring threads read neighbouring values (rows of any length: 8.8
-// -> 4.2 us at 37 x 2047 float32 against 8 neighbours).
+// -> 4.6 us at 37 x 2047 float32 against 8 neighbours).
 enum NormLayout { kWide, kNeighbours, kApart };
 
 // Values e0, e0 + es, .. of a row as floats; those at or past D read as 0.
@@ -66,7 +75,7 @@ __device__ __forceinline__ void norm_load_w(const void* w, bool w_bf16, size_t o
 }
 
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(bf16_t* p, float v) { *p = (bf16_t)bf16_bits(v); }
+__device__ __forceinline__ void put(bf16_t* p, float v) { *p = bf16_bits(v); }
 
 template <typename T, int LAYOUT>
 __device__ __forceinline__ void norm_store(T* row, int e0, int es, int D, const float* v) {
@@ -77,10 +86,10 @@ __device__ __forceinline__ void norm_store(T* row, int e0, int es, int D, const 
       *reinterpret_cast<float4*>(row + e0 + 4) = make_float4(v[4], v[5], v[6], v[7]);
     } else {
       uint4 w;
-      w.x = bf16_bits(v[0]) | bf16_bits(v[1]) << 16;
-      w.y = bf16_bits(v[2]) | bf16_bits(v[3]) << 16;
-      w.z = bf16_bits(v[4]) | bf16_bits(v[5]) << 16;
-      w.w = bf16_bits(v[6]) | bf16_bits(v[7]) << 16;
+      w.x = bf16_pair(v[0], v[1]);
+      w.y = bf16_pair(v[2], v[3]);
+      w.z = bf16_pair(v[4], v[5]);
+      w.w = bf16_pair(v[6], v[7]);
       *reinterpret_cast<uint4*>(row + e0) = w;
     }
   } else {
@@ -90,17 +99,33 @@ __device__ __forceinline__ void norm_store(T* row, int e0, int es, int D, const 
   }
 }
 
+// Sum over each row of 16 lanes, the same bits in all of them: every step adds
+// two partial sums that both lanes hold.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += dpp_f32<0xb1>(v);
+  v += dpp_f32<0x4e>(v);
+  v += dpp_f32<0x141>(v);
+  return v + dpp_f32<0x140>(v);
+}
+
 // Sum over the workgroup, the same value in every thread.  Two calls use two
 // arrays, so the second needs no barrier before it.
+static_assert(kNormMaxThreads / kWave <= 16, "a row of lanes sums the waves");
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = wave_sum(v);
-  const int nw = blockDim.x / kWave;
+  const int nw = blockDim.x / kWave, i = threadIdx.x % 16;
   if (nw == 1) return v;
   if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = v;
   __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < nw; ++i) s += red[i];
-  return s;
+  return row16_sum(i < nw ? red[i] : 0.f);
+}
+
+// 1 / sqrt(v) for v >= 0.  The instruction is within a step of it, but takes
+// subnormal numbers as 0.
+__device__ __forceinline__ float inv_root(float v) {
+  const bool tiny = v < 0x1p-100f;
+  const float r = __builtin_amdgcn_rsqf(tiny ? v * 0x1p100f : v);
+  return tiny ? r * 0x1p50f : r;
 }
 
 // Rows of more than 2 groups per thread leave the residual in memory until
@@ -137,7 +162,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void hidden_norm_kernel(NormArgs a
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
-    f = a.scale / sqrtf(block_sum(ss, red[0]) / (float)D + a.eps);
+    f = a.scale * inv_root(fmaf(block_sum(ss, red[0]), a.inv_d, a.eps));
   }
   float ss = 0.f;
 #pragma unroll
@@ -163,7 +188,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void hidden_norm_kernel(NormArgs a
     }
     norm_store<R, LAYOUT>(static_cast<R*>(a.r_out) + off, e0, es, D, h[j]);
   }
-  f = 1.f / sqrtf(block_sum(ss, red[1]) / (float)D + a.eps);
+  f = inv_root(fmaf(block_sum(ss, red[1]), a.inv_d, a.eps));
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e0 = at(j);
@@ -232,6 +257,7 @@ hipError_t launch_hidden_norm(const void* x, bool xb, const void* r, bool rb, co
   a.w_bf16 = wb;
   a.scale = scale;
   a.eps = eps;
+  a.inv_d = 1.f / (float)D;
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   const bool vec = D % 8 == 0 && al(x) && al(r) && al(w1) && al(gate) && al(w2) && al(r_out) &&
                    (out_dtype == SPECV_OUT_E4M3 || al(out));
