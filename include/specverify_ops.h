@@ -69,7 +69,8 @@ typedef enum {
  * M >= 1, 1 <= D <= SPECV_MAX_D.  Arrays element-aligned; with 16-byte aligned
  * arrays and D a multiple of 8 all loads are 16 bytes wide; e4m3 output needs
  * out 8-byte aligned.  Outputs may not overlap inputs or each other but for
- * the two cases above.  Sums in float32.  A NaN or an infinity in a row
+ * the two cases above.  Sums in float32: a row of x or r' whose sum of squares
+ * passes the largest float is scaled by 0.  A NaN or an infinity in a row
  * makes NaN of that row's y at least where it stands (a whole run of 128 with
  * SPECV_OUT_E4M3); other rows are not affected.
  */
@@ -132,7 +133,10 @@ SPECV_OPS_API specv_status_t specv_fp8_lm_head_pack_weight(const uint8_t *q, con
  *  logits         [M][V] of out_dtype, output; not overlapping the inputs.
  * M >= 1, 1 <= V <= SPECV_MAX_V, D a positive multiple of 128 up to
  * SPECV_MAX_D.  A NaN byte (element or scale) in a hidden row makes that row
- * of logits NaN, one in a weight row that vocabulary id.
+ * of logits NaN, one in a weight row that vocabulary id.  Float32 logits take
+ * each value, element times scale, as a bfloat16 number: one below 2^-126 in
+ * size may count as 0, one past the largest float as infinite (scale bytes
+ * below 10 or above 246 alone can make such values).
  */
 SPECV_OPS_API specv_status_t specv_fp8_lm_head(const uint8_t *hidden, const uint8_t *hidden_scale,
                                                const void *packed_weight, int M, int D, int V,

@@ -419,11 +419,12 @@ __global__ __launch_bounds__(kProbOneThreads) void prob_one_kernel(ProbArgs a) {
   prob_outputs(a, b, lane, s, y, mass);
 }
 
-// Largest vocabulary the one-kernel form takes.
-#ifndef SPECV_ONE_V
-#define SPECV_ONE_V 32768
-#endif
-constexpr int kProbOneV = SPECV_ONE_V;
+// Largest vocabulary the one-kernel form takes.  One kernel against two, us a
+// call: 1 x 4096 4.5 / 6.6, 1 x 32000 7.4 / 7.4, 64 x 32000 9.7 / 10.7, then
+// 1 x 65000 9.6 / 7.5 and 64 x 65000 15.2 / 12.8 (float32, 5 and 4 drafts): past
+// some 32000 values one workgroup's pass over its row takes longer than a second
+// launch and its wait.
+constexpr int kProbOneV = 32768;
 static_assert(kProbOneV <= kProbOneChunks * kProbChunk, "records fit LDS");
 
 // 0: the one-kernel form needs none.

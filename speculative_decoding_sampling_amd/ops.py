@@ -99,12 +99,18 @@ def _load_native():
 
 def _raw_stream(t, stream):
     """The raw handle of ``stream``, by default the current one of the tensor's
-    device; 0 for a tensor that the call will refuse."""
+    device; 0 for a tensor that the call will refuse.  Another stream than the
+    current one first waits for it: the outputs are allocated on the current
+    stream, whose pending work may still use their memory."""
     index = t.get_device() if isinstance(t, torch.Tensor) else -1
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0
     if index >= 0 and stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    if index >= 0:
+        current = torch.cuda.current_stream(t.device)
+        if current != stream:
+            stream.wait_stream(current)
     return stream.cuda_stream
 
 
