@@ -30,6 +30,8 @@
 extern "C" {
 #endif
 
+/* Sizes whose launch would take 2^32 or more threads are SPECV_EUNSUPPORTED. */
+
 /* Values that share one scale in the 8-bit formats below. */
 #define SPECV_FP8_BLOCK 128
 
@@ -191,6 +193,8 @@ SPECV_OPS_API specv_status_t specv_verify_fp8_lm_head(
  *                none: the size is then 0 (as for sizes the call refuses).
  *  accept_prob, residual_mass, stop_pos, path: nullable diagnostics, as for
  *                specv_verify_debug.
+ *
+ * Outputs and workspace do not overlap the inputs or each other.
  *
  * 1 <= B, 0 <= K <= SPECV_MAX_K, 1 <= V <= SPECV_MAX_V.  Per-request errors
  * as specv_verify (draft_len, a token or a uniform out of range, q(x) not

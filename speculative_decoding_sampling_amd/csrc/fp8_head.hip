@@ -19,6 +19,7 @@
 // one run, so a lane's scale byte is that of its row and run whatever the
 // matrix core's own 32-wide blocks are.
 #include "fp8.h"
+#include "grid.h"
 #include "specverify_ops.h"
 
 namespace specv {
@@ -67,12 +68,12 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(const T* __restrict__
   }
 }
 
+bool fp8_quantize_fits(int rows, int D) { return grid_fits(((size_t)rows * D / 8 + 255) / 256, 256); }
+
 hipError_t launch_fp8_quantize(const void* x, bool bf16, int rows, int D, uint8_t* q,
                                uint8_t* scale, hipStream_t stream) {
   const size_t n8 = (size_t)rows * D / 8;
-  const size_t blocks = (n8 + 255) / 256;
-  if (blocks > 0x7fffffffu) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks);
+  const dim3 grid((unsigned)((n8 + 255) / 256));
   if (bf16)
     fp8_quantize_kernel<<<grid, dim3(256), 0, stream>>>(static_cast<const bf16_t*>(x), n8, q, scale);
   else
@@ -115,12 +116,16 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const uint8_t* __restrict
   }
 }
 
+bool fp8_pack_fits(int V, int D) {
+  const size_t pieces = fp8_packed_scale_off(V, D) / 16;
+  return grid_fits((pieces + (fp8_packed_bytes(V, D) - pieces * 16) / 4 + 255) / 256, 256);
+}
+
 hipError_t launch_fp8_pack(const uint8_t* q, const uint8_t* scale, void* packed, int V, int D,
                            hipStream_t stream) {
   const size_t pieces = fp8_packed_scale_off(V, D) / 16;
   const size_t words = (fp8_packed_bytes(V, D) - pieces * 16) / 4;
   const size_t blocks = (pieces + words + 255) / 256;
-  if (blocks > 0x7fffffffu) return hipErrorInvalidConfiguration;
   fp8_pack_kernel<<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(
       q, scale, static_cast<uint8_t*>(packed), V, D, pieces, words);
   return hipGetLastError();
@@ -520,7 +525,6 @@ hipError_t fp8_tiles(const Fp8Args& a, O* out) {
   const int nrb = (a.M + 32 * MT - 1) / (32 * MT);
   const size_t nwork = (size_t)((a.V + kTileVocab - 1) / kTileVocab) * nrb;
   const size_t blocks = (nwork + kXcds - 1) / kXcds * kXcds;
-  if (blocks > 0x7fffffffu) return hipErrorInvalidConfiguration;
   fp8_tile_kernel<MT, RING, ONCE, O><<<dim3((unsigned)blocks), dim3(kF8Threads), 0, a.stream>>>(
       a.H, a.hs, a.P, reinterpret_cast<const uint32_t*>(a.ws), a.M, a.D, a.V, fp8_groups(a.V), nrb,
       (int)nwork, out);
@@ -531,7 +535,6 @@ template <bool ONCE, typename O>
 hipError_t fp8_skinny(const Fp8Args& a, O* out) {
   const int ng = fp8_groups(a.V);
   const size_t blocks = (size_t)ng * ((a.M + 31) / 32);
-  if (blocks > 0x7fffffffu) return hipErrorInvalidConfiguration;
   fp8_skinny_kernel<ONCE, O><<<dim3((unsigned)blocks), dim3(kF8Threads), 0, a.stream>>>(
       a.H, a.hs, a.P, a.ws, a.M, a.D, a.V, ng, out);
   return hipGetLastError();
@@ -601,7 +604,9 @@ hipError_t launch_fp8_head(const uint8_t* hidden, const uint8_t* hscale, const v
   return bf16 ? fp8_head(a, static_cast<bf16_t*>(logits)) : fp8_head(a, static_cast<float*>(logits));
 }
 
-// Largest grid of any product (workgroups), for the host's size check.
-size_t fp8_head_blocks(int M, int V) { return (size_t)fp8_groups(V) * ((M + 31) / 32); }
+// Whether a product's grid fits, by the one with the most workgroups.
+bool fp8_head_fits(int M, int V) {
+  return grid_fits((size_t)fp8_groups(V) * ((M + 31) / 32), kF8Threads);
+}
 
 }  // namespace specv

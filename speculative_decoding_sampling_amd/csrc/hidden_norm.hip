@@ -22,6 +22,7 @@
 // y is formed from r' before r' is rounded to its own type: one rounding less
 // between the residual stream and the logits.
 #include "fp8.h"
+#include "grid.h"
 #include "specverify_ops.h"
 
 namespace specv {
@@ -220,11 +221,15 @@ void norm_launch(const NormArgs& a, int M, int threads, bool vec, hipStream_t st
   else hidden_norm_kernel<X, R, OUT, NV, kNarrow><<<dim3(M), dim3(threads), 0, stream>>>(a);
 }
 
+int norm_threads(int D) {
+  const int groups = (D + 7) / 8;
+  return groups >= kNormMaxThreads ? kNormMaxThreads : (groups + kWave - 1) / kWave * kWave;
+}
+bool hidden_norm_fits(int M, int D) { return grid_fits(M, norm_threads(D)); }
+
 template <typename X, typename R, int OUT>
 void norm_by_size(const NormArgs& a, int M, bool vec, hipStream_t stream) {
-  const int groups = (a.D + 7) / 8;
-  const int threads = groups >= kNormMaxThreads ? kNormMaxThreads
-                                                : (groups + kWave - 1) / kWave * kWave;
+  const int groups = (a.D + 7) / 8, threads = norm_threads(a.D);
   const int nv = (groups + threads - 1) / threads;
   if (nv == 1) norm_launch<X, R, OUT, 1>(a, M, threads, vec, stream);
   else if (nv == 2) norm_launch<X, R, OUT, 2>(a, M, threads, vec, stream);

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 namespace specv {
+bool probs_fits(int B, int V);
 size_t probs_workspace_bytes(int B, int V);
 hipError_t launch_verify_probs(bool bf16, const void* tgt, long long tsb, long long tsk,
                                const void* dft, long long dsb, long long dsk, const int* tokens,
@@ -14,16 +15,19 @@ hipError_t launch_verify_probs(bool bf16, const void* tgt, long long tsb, long l
                                int K, int V, int eos_id, int* out_tokens, int* n_emitted,
                                void* workspace, float* alpha_out, double* rmass_out, int* stop_out,
                                int* path_out, hipStream_t stream);
+bool hidden_norm_fits(int M, int D);
 hipError_t launch_hidden_norm(const void* x, bool xb, const void* r, bool rb, const void* w1,
                               const void* gate, int gate_rows, const void* w2, bool wb, int M,
                               int D, float scale, float eps, void* r_out, void* out, int out_dtype,
                               uint8_t* out_scale, hipStream_t stream);
+bool fp8_quantize_fits(int rows, int D);
 hipError_t launch_fp8_quantize(const void* x, bool bf16, int rows, int D, uint8_t* q,
                                uint8_t* scale, hipStream_t stream);
 size_t fp8_packed_bytes(int V, int D);
 hipError_t launch_fp8_pack(const uint8_t* q, const uint8_t* scale, void* packed, int V, int D,
                            hipStream_t stream);
-size_t fp8_head_blocks(int M, int V);
+bool fp8_head_fits(int M, int V);
+bool fp8_pack_fits(int V, int D);
 hipError_t launch_fp8_head(const uint8_t* hidden, const uint8_t* hscale, const void* packed, int M,
                            int D, int V, void* logits, bool bf16, hipStream_t stream);
 
@@ -50,14 +54,14 @@ specv_status_t status(hipError_t e) { return e == hipSuccess ? SPECV_OK : SPECV_
 specv_status_t check_head_sizes(int M, int D, int V) {
   if (M < 1 || V < 1 || D < 1 || D % SPECV_FP8_BLOCK != 0) return SPECV_EINVAL;
   if (V > SPECV_MAX_V || D > SPECV_MAX_D) return SPECV_EUNSUPPORTED;
-  if (fp8_head_blocks(M, V) > 0x7fffffffu) return SPECV_EUNSUPPORTED;
+  if (!fp8_head_fits(M, V) || !fp8_pack_fits(V, D)) return SPECV_EUNSUPPORTED;
   return SPECV_OK;
 }
 
 specv_status_t check_probs_sizes(int B, int K, int V) {
   if (B < 1 || K < 0 || K > SPECV_MAX_K || V < 1) return SPECV_EINVAL;
   if (V > SPECV_MAX_V) return SPECV_EUNSUPPORTED;
-  if ((size_t)B * ((V + 1023) / 1024) > 0x7fffffffu) return SPECV_EUNSUPPORTED;
+  if (!probs_fits(B, V)) return SPECV_EUNSUPPORTED;
   return SPECV_OK;
 }
 
@@ -74,7 +78,7 @@ specv_status_t specv_hidden_norm(const void* x, specv_dtype_t x_dtype, const voi
                                  uint8_t* out_scale, hipStream_t stream) {
   using namespace specv;
   if (M < 1 || D < 1) return SPECV_EINVAL;
-  if (D > SPECV_MAX_D) return SPECV_EUNSUPPORTED;
+  if (D > SPECV_MAX_D || !hidden_norm_fits(M, D)) return SPECV_EUNSUPPORTED;
   if (!known(x_dtype) || !known(residual_dtype) || !known(weight_dtype)) return SPECV_EINVAL;
   const bool fp8 = out_dtype == SPECV_OUT_E4M3;
   if (!fp8 && out_dtype != SPECV_OUT_F32 && out_dtype != SPECV_OUT_BF16) return SPECV_EINVAL;
@@ -113,7 +117,7 @@ specv_status_t specv_fp8_quantize(const void* x, specv_dtype_t dtype, int rows, 
                                   uint8_t* scale, hipStream_t stream) {
   using namespace specv;
   if (rows < 1 || D < 1 || D % SPECV_FP8_BLOCK != 0 || !known(dtype)) return SPECV_EINVAL;
-  if (D > SPECV_MAX_D) return SPECV_EUNSUPPORTED;
+  if (D > SPECV_MAX_D || !fp8_quantize_fits(rows, D)) return SPECV_EUNSUPPORTED;
   if (!x || !q || !scale || misaligned(x, 16) || misaligned(q, 8)) return SPECV_EINVAL;
   const size_t n = (size_t)rows * D;
   const Span in = {x, n * size_of(dtype)}, o = {q, n}, s = {scale, n / SPECV_FP8_BLOCK};
@@ -239,7 +243,19 @@ specv_status_t specv_verify_probs(const void* target_probs, int64_t target_strid
       misaligned(accept_prob, 4) || misaligned(residual_mass, 8) || misaligned(stop_pos, 4) ||
       misaligned(path, 4))
     return SPECV_EINVAL;
-  const size_t need = probs_workspace_bytes(B, V);
+  // the waves of a request read its inputs while one of them writes its outputs
+  const size_t need = probs_workspace_bytes(B, V), nk = (size_t)B * K;
+  const Span in[4] = {{K > 0 ? draft_tokens : nullptr, nk * 4}, {draft_len, (size_t)B * 4},
+                      {K > 0 ? u : nullptr, nk * 4}, {u_final, (size_t)B * 4}};
+  const Span o[7] = {{out_tokens, (nk + B) * 4}, {n_emitted, (size_t)B * 4}, {accept_prob, nk * 4},
+                     {residual_mass, (size_t)B * 8}, {stop_pos, (size_t)B * 4},
+                     {path, (size_t)B * 4}, {need > 0 ? workspace : nullptr, need}};
+  for (int i = 0; i < 7; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (overlap(o[i], in[j])) return SPECV_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(o[i], o[j])) return SPECV_EINVAL;
+  }
   if (need > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
     return SPECV_EWORKSPACE;
   return status(launch_verify_probs(dtype == SPECV_BF16, target_probs, target_stride_b,

@@ -21,6 +21,7 @@
 // sums to the chunk that holds the draw and scans that chunk.  Small
 // vocabularies do both in one workgroup per request, the chunk sums in LDS.
 #include "common.h"
+#include "grid.h"
 #include "specverify.h"
 #include "wave_scan.h"
 
@@ -427,6 +428,14 @@ __global__ __launch_bounds__(kProbOneThreads) void prob_one_kernel(ProbArgs a) {
 constexpr int kProbOneV = 32768;
 static_assert(kProbOneV <= kProbOneChunks * kProbChunk, "records fit LDS");
 
+// Whether the launches of a call fit.
+bool probs_fits(int B, int V) {
+  if (V <= kProbOneV) return grid_fits(B, kProbOneThreads);
+  const size_t nch = (size_t)((V + kProbChunk - 1) / kProbChunk);
+  const size_t waves = kProbPassThreads / kWave;
+  return grid_fits(B * ((nch + waves - 1) / waves), kProbPassThreads);
+}
+
 // 0: the one-kernel form needs none.
 size_t probs_workspace_bytes(int B, int V) {
   if (V <= kProbOneV) return 0;
@@ -470,7 +479,6 @@ hipError_t launch_verify_probs(bool bf16, const void* tgt, long long tsb, long l
   }
   constexpr int kWaves = kProbPassThreads / kWave;
   const int nblk = (a.nch + kWaves - 1) / kWaves;
-  if ((size_t)B * nblk > 0x7fffffffu) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)((size_t)B * nblk));
   if (bf16) {
     prob_pass_kernel<bf16_t><<<grid, dim3(kProbPassThreads), 0, stream>>>(a, nblk);

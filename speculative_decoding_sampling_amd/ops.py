@@ -231,6 +231,8 @@ def verify_fp8_lm_head(hidden, hidden_scale, packed, draft_logits, draft_tokens,
 
 def _round_workspace(hidden, V, D, top_k, top_p, stream):
     """Workspace of a fused round, allocated on the stream that will use it."""
+    if not isinstance(hidden, torch.Tensor):
+        raise TypeError("hidden must be a torch.Tensor")
     if hidden.dim() != 3 or not hidden.is_cuda:
         raise ValueError("hidden must be a [B, K+1, D] GPU tensor")
     B, K = hidden.shape[0], hidden.shape[1] - 1
@@ -264,7 +266,7 @@ def verify_probs(target_probs, draft_probs, draft_tokens, draft_len, u, u_final,
     ``residual_mass``, ``stop_pos`` and ``path`` when ``debug`` is true, all as
     ``binding.verify`` gives them.  Asynchronous on ``stream``."""
     raw = _raw_stream(target_probs, stream)
-    if stream is not None and workspace is None and target_probs.dim() == 3:
+    if raw and stream is not None and workspace is None and target_probs.dim() == 3:
         # allocated on the stream that uses it: it is given back right after
         B, K1, V = target_probs.shape
         with torch.cuda.stream(stream):
