@@ -243,8 +243,10 @@ specv_status_t specv_verify_probs(const void* target_probs, int64_t target_strid
       misaligned(accept_prob, 4) || misaligned(residual_mass, 8) || misaligned(stop_pos, 4) ||
       misaligned(path, 4))
     return SPECV_EINVAL;
-  // the waves of a request read its inputs while one of them writes its outputs
   const size_t need = probs_workspace_bytes(B, V), nk = (size_t)B * K;
+  if (need > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
+    return SPECV_EWORKSPACE;
+  // the waves of a request read its inputs while one of them writes its outputs
   const Span in[4] = {{K > 0 ? draft_tokens : nullptr, nk * 4}, {draft_len, (size_t)B * 4},
                       {K > 0 ? u : nullptr, nk * 4}, {u_final, (size_t)B * 4}};
   const Span o[7] = {{out_tokens, (nk + B) * 4}, {n_emitted, (size_t)B * 4}, {accept_prob, nk * 4},
@@ -256,8 +258,6 @@ specv_status_t specv_verify_probs(const void* target_probs, int64_t target_strid
     for (int j = 0; j < i; ++j)
       if (overlap(o[i], o[j])) return SPECV_EINVAL;
   }
-  if (need > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
-    return SPECV_EWORKSPACE;
   return status(launch_verify_probs(dtype == SPECV_BF16, target_probs, target_stride_b,
                                     target_stride_k, draft_probs, draft_stride_b, draft_stride_k,
                                     draft_tokens, draft_len, u, u_final, B, K, V, eos_id,
