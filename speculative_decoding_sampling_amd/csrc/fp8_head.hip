@@ -322,26 +322,32 @@ constexpr int kTileGroups = kTileVocab / kF8Group;
 constexpr int kXcds = 8;
 static_assert(kTileGroups == 2 * kF8Waves, "two packed groups to a wave");
 
-template <int MT, int RING, bool ONCE, typename O>
-__global__ __launch_bounds__(kF8Threads, 2) void fp8_tile_kernel(
-    const uint8_t* __restrict__ H, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ P,
-    const uint32_t* __restrict__ ws, int M, int D, int V, int ngroup, int nrb, int nwork,
-    O* __restrict__ out) {
-  constexpr int kRows = MT * 32;
-  constexpr int kBuf = kRows * kFp8Block;
-  static_assert(kRows <= kF8Threads, "one row's scales to a thread");
-  // epilogue: 32 rows of bfloat16 or 16 of float32 at a time, in the run buffers
-  constexpr int kTrStride = kTileVocab + 16 / (int)sizeof(O);
-  constexpr int kTrRows = 64 / (int)sizeof(O);
-  constexpr int kTrBytes = kTrRows * kTrStride * (int)sizeof(O);
-  static_assert(4 % RING == 0, "the weight ring indexes statically over a group of runs");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuf > kTrBytes ? 2 * kBuf : kTrBytes];
-  __shared__ uint32_t lsc[2][kF8Threads];                    // words past kRows are not read
+// A tile's LDS: two runs of staged hidden rows, in whose place the epilogue
+// moves 32 rows of bfloat16 logits or 16 of float32 at a time; two words of the
+// rows' scales.
+template <int MT, typename O>
+struct Fp8Tile {
+  static constexpr int kRows = MT * 32;
+  static constexpr int kBuf = kRows * kFp8Block;
+  static constexpr int kTrStride = kTileVocab + 16 / (int)sizeof(O);
+  static constexpr int kTrRows = 64 / (int)sizeof(O);
+  static constexpr int kTrBytes = kTrRows * kTrStride * (int)sizeof(O);
+  static constexpr int kBytes = 2 * kBuf > kTrBytes ? 2 * kBuf : kTrBytes;
+  static constexpr int kRing = MT <= 2 ? 4 : 2;              // runs of weights in registers
+};
 
-  const int per = (nwork + kXcds - 1) / kXcds;
-  const int work = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
-  if (work >= nwork) return;                                 // blockIdx.x / kXcds < per
-  const int tile = work / nrb, m0 = (work % nrb) * kRows;
+// The tile of 256 vocabulary ids and hidden rows m0 .. m0 + 32 MT - 1.
+template <int MT, bool ONCE, typename O>
+__device__ __forceinline__ void fp8_tile(uint8_t* lds, uint32_t (&lsc)[2][kF8Threads],
+                                         const uint8_t* __restrict__ H,
+                                         const uint8_t* __restrict__ hs,
+                                         const uint8_t* __restrict__ P,
+                                         const uint32_t* __restrict__ ws, int M, int D, int V,
+                                         int ngroup, int tile, int m0, O* __restrict__ out) {
+  using T = Fp8Tile<MT, O>;
+  constexpr int kBuf = T::kBuf, kTrStride = T::kTrStride, kTrRows = T::kTrRows, RING = T::kRing;
+  static_assert(T::kRows <= kF8Threads, "one row's scales to a thread");
+  static_assert(4 % RING == 0, "the weight ring indexes statically over a group of runs");
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int h = lane / 32, l32 = lane % 32;
@@ -514,18 +520,43 @@ __global__ __launch_bounds__(kF8Threads, 2) void fp8_tile_kernel(
     }
 }
 
+// The last row block is a tile of the 32-row steps that it has (bfloat16, us: 320
+// x 128256 x 4096 219 -> 212, 200 rows 156 -> 150, 160 x 64000 x 4096 75 -> 66
+// against whole tiles).
+template <int MT, bool ONCE, typename O>
+__global__ __launch_bounds__(kF8Threads, 2) void fp8_tile_kernel(
+    const uint8_t* __restrict__ H, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ P,
+    const uint32_t* __restrict__ ws, int M, int D, int V, int ngroup, int nrb, int nwork,
+    O* __restrict__ out) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Fp8Tile<MT, O>::kBytes];
+  __shared__ uint32_t lsc[2][kF8Threads];                    // words past the rows are not read
+  const int per = (nwork + kXcds - 1) / kXcds;
+  const int work = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
+  if (work >= nwork) return;                                 // blockIdx.x / kXcds < per
+  const int tile = work / nrb, m0 = (work % nrb) * 32 * MT;
+  const int steps = (M - m0 + 31) / 32;
+  if (MT > 3 && steps == 3)
+    fp8_tile<MT < 3 ? MT : 3, ONCE>(lds, lsc, H, hs, P, ws, M, D, V, ngroup, tile, m0, out);
+  else if (MT > 2 && steps == 2)
+    fp8_tile<MT < 2 ? MT : 2, ONCE>(lds, lsc, H, hs, P, ws, M, D, V, ngroup, tile, m0, out);
+  else if (MT > 1 && steps == 1)
+    fp8_tile<1, ONCE>(lds, lsc, H, hs, P, ws, M, D, V, ngroup, tile, m0, out);
+  else
+    fp8_tile<MT, ONCE>(lds, lsc, H, hs, P, ws, M, D, V, ngroup, tile, m0, out);
+}
+
 struct Fp8Args {
   const uint8_t *H, *hs, *P, *ws;
   int M, D, V;
   hipStream_t stream;
 };
 
-template <int MT, int RING, bool ONCE, typename O>
+template <int MT, bool ONCE, typename O>
 hipError_t fp8_tiles(const Fp8Args& a, O* out) {
   const int nrb = (a.M + 32 * MT - 1) / (32 * MT);
   const size_t nwork = (size_t)((a.V + kTileVocab - 1) / kTileVocab) * nrb;
   const size_t blocks = (nwork + kXcds - 1) / kXcds * kXcds;
-  fp8_tile_kernel<MT, RING, ONCE, O><<<dim3((unsigned)blocks), dim3(kF8Threads), 0, a.stream>>>(
+  fp8_tile_kernel<MT, ONCE, O><<<dim3((unsigned)blocks), dim3(kF8Threads), 0, a.stream>>>(
       a.H, a.hs, a.P, reinterpret_cast<const uint32_t*>(a.ws), a.M, a.D, a.V, fp8_groups(a.V), nrb,
       (int)nwork, out);
   return hipGetLastError();
@@ -563,7 +594,9 @@ int fp8_choice(int M, int D, int V, bool exact) {
     const int nrb = (M + 32 * mt - 1) / (32 * mt);
     const double cus = tiles * nrb / 256;
     const double load = cus <= 1 ? 1 : cus <= 1.55 ? 1.55 : cus < 3 ? 1.12 * cus : cus;
-    const double work = load * runs * run_ns[mt] * (exact ? 1.6 : 1);
+    const int last = (M - 32 * mt * (nrb - 1) + 31) / 32;      // 32-row steps of the last block
+    const double mean = ((nrb - 1) * run_ns[mt] + run_ns[last]) / nrb;
+    const double work = load * runs * mean * (exact ? 1.6 : 1);
     double rate = nrb == 1 ? 5400 : 4300;
     if (rate > 34 * tiles * nrb) rate = 34 * tiles * nrb;
     const double t = 3000 + (work > bytes / rate ? work : bytes / rate);
@@ -583,11 +616,11 @@ int fp8_choice(int M, int D, int V, bool exact) {
 template <bool ONCE, typename O>
 hipError_t fp8_run(const Fp8Args& a, int choice, O* out) {
   if (choice == 0) return fp8_skinny<ONCE>(a, out);
-  if (choice == 1) return fp8_tiles<1, 4, ONCE>(a, out);
-  if (choice == 2) return fp8_tiles<2, 4, ONCE>(a, out);
+  if (choice == 1) return fp8_tiles<1, ONCE>(a, out);
+  if (choice == 2) return fp8_tiles<2, ONCE>(a, out);
   if constexpr (!kFp8Exact<O>)                               // float32: 4 would spill
-    if (choice == 4) return fp8_tiles<4, 2, ONCE>(a, out);
-  return fp8_tiles<3, 2, ONCE>(a, out);
+    if (choice == 4) return fp8_tiles<4, ONCE>(a, out);
+  return fp8_tiles<3, ONCE>(a, out);
 }
 template <typename O>
 hipError_t fp8_head(const Fp8Args& a, O* out) {
