@@ -178,7 +178,8 @@ __device__ __forceinline__ void prob_load(const T* __restrict__ row, int base, i
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int v = STRIPED ? base + (j * kWave + lane) * N + i : base + lane * kProbPer + j * N + i;
-        out[j * N + i] = v < V ? to_f32(row[v]) : 0.f;
+        const float p = to_f32(row[min(v, V - 1)]);         // no branch: all loads in flight
+        out[j * N + i] = v < V ? p : 0.f;
       }
   }
 }
@@ -292,9 +293,9 @@ __device__ __forceinline__ void prob_error(const ProbArgs& a, int b, int lane) {
   prob_outputs(a, b, lane, e, -1, 0.0);
 }
 
-// A walk over chunk sums, 64 at a time: rec(c), called by the whole wave, is
-// lane l's sum of chunk c = 64 i + l (0 past the last).  Lane i keeps the total
-// of batch i.
+// A walk over chunk sums, 64 at a time: rec(i), called by the whole wave, is
+// lane l's sum of chunk 64 i + l (0 past the last).  Lane i keeps the total of
+// batch i.
 struct ProbWalk {
   double batch, total;
 };
@@ -302,7 +303,7 @@ template <typename F>
 __device__ __forceinline__ ProbWalk prob_total(int nch, int lane, F rec) {
   double mine = 0.0;
   for (int i = 0; i * kProbBatch < nch; ++i) {
-    const double s = wave_sum(rec(i * kProbBatch + lane));
+    const double s = wave_sum(rec(i));
     if (lane == i) mine = s;
   }
   return {mine, wave_sum(mine)};
@@ -314,22 +315,21 @@ __device__ __forceinline__ int prob_find(const ProbWalk& w, int lane, double t, 
   const double bincl = wave_incl_scan(w.batch);
   const int bi = prob_lane(bincl, w.batch, t);
   const double start = lane_value(wave_shr1(bincl), bi);
-  const double r = rec(bi * kProbBatch + lane);
+  const double r = rec(bi);
   const double cincl = start + wave_incl_scan(r);
   const int ci = prob_lane(cincl, r, t);
   before = ci ? lane_value(cincl, ci - 1) : start;
   return bi * kProbBatch + ci;
 }
 
-// The draw of a planned request from its chunk records, by one wave: the
-// token, -1 where an entry is invalid or there is no mass.
-template <typename T>
+// The draw of a planned request from its chunk records, a walk over them and
+// their access, by one wave: the token, -1 where an entry is invalid or there is
+// no mass.
+template <typename T, typename F>
 __device__ __forceinline__ int prob_pick(const ProbArgs& a, int b, int lane, const ProbPlan& s,
-                                         const double* recs, double& mass) {
+                                         const ProbWalk& w, F rec, double& mass) {
   ProbRows<T> rows = prob_rows<T>(a, b, s);
   double before;
-  auto rec = [&](int c) { return c < a.nch ? recs[c] : 0.0; };
-  const ProbWalk w = prob_total(a.nch, lane, rec);
   mass = s.path == kPathReject ? w.total : 0.0;
   if (w.total > 0.0) {
     const double t = (double)s.uf * w.total;
@@ -342,10 +342,10 @@ __device__ __forceinline__ int prob_pick(const ProbArgs& a, int b, int lane, con
   // probabilities leads here).
   rows.q = nullptr;
   rows.hot = -1;
-  auto sum = [&](int c) {
+  auto sum = [&](int i) {
     double mine = 0.0;
-    for (int l = 0; l < kProbBatch && c - lane + l < a.nch; ++l) {
-      const double v = prob_chunk<T>(rows, c - lane + l, lane, a.V);
+    for (int l = 0; l < kProbBatch && i * kProbBatch + l < a.nch; ++l) {
+      const double v = prob_chunk<T>(rows, i * kProbBatch + l, lane, a.V);
       if (lane == l) mine = v;
     }
     return mine;
@@ -376,14 +376,38 @@ __global__ __launch_bounds__(kProbPassThreads) void prob_pass_kernel(ProbArgs a,
   }
 }
 
-// The draws: one wave per request.
-template <typename T>
+// The draws: one wave per request.  HELD: up to four batches of records are
+// fetched at once, beside the plan, and kept in registers for both walks.  (Four
+// variables: an array that is indexed at run time leaves the registers.)
+constexpr int kProbHeld = 4;
+template <typename T, bool HELD>
 __global__ __launch_bounds__(kWave) void prob_draw_kernel(ProbArgs a) {
   const int b = blockIdx.x, lane = threadIdx.x;
+  const double* recs = a.recs + (size_t)b * a.nch;
+  auto load = [&](int i) {
+    const int c = i * kProbBatch + lane;
+    const double v = recs[min(c, a.nch - 1)];
+    return c < a.nch ? v : 0.0;
+  };
+  double h0 = 0.0, h1 = 0.0, h2 = 0.0, h3 = 0.0;
+  if constexpr (HELD) {
+    h0 = load(0);
+    h1 = load(1);
+    h2 = load(2);
+    h3 = load(3);
+  }
   const ProbPlan p = a.plans[b];
   if (!prob_draws(p.path)) return;
   double mass;
-  const int y = prob_pick<T>(a, b, lane, p, a.recs + (size_t)b * a.nch, mass);
+  int y;
+  if constexpr (HELD) {
+    const double s0 = wave_sum(h0), s1 = wave_sum(h1), s2 = wave_sum(h2), s3 = wave_sum(h3);
+    const double batch = lane == 0 ? s0 : lane == 1 ? s1 : lane == 2 ? s2 : lane == 3 ? s3 : 0.0;
+    auto rec = [=](int i) { return i == 0 ? h0 : i == 1 ? h1 : i == 2 ? h2 : h3; };
+    y = prob_pick<T>(a, b, lane, p, {batch, wave_sum(batch)}, rec, mass);
+  } else {
+    y = prob_pick<T>(a, b, lane, p, prob_total(a.nch, lane, load), load, mass);
+  }
   if (y < 0) {
     prob_error(a, b, lane);
   } else if (lane == 0) {
@@ -411,7 +435,8 @@ __global__ __launch_bounds__(kProbOneThreads) void prob_one_kernel(ProbArgs a) {
   int y = -1;
   double mass = 0.0;
   if (prob_draws(s.path)) {
-    y = prob_pick<T>(a, b, lane, p, recs, mass);
+    auto rec = [&](int i) { return i * kProbBatch + lane < a.nch ? recs[i * kProbBatch + lane] : 0.0; };
+    y = prob_pick<T>(a, b, lane, p, prob_total(a.nch, lane, rec), rec, mass);
     if (y < 0) {
       prob_error(a, b, lane);
       return;
@@ -480,13 +505,12 @@ hipError_t launch_verify_probs(bool bf16, const void* tgt, long long tsb, long l
   constexpr int kWaves = kProbPassThreads / kWave;
   const int nblk = (a.nch + kWaves - 1) / kWaves;
   const dim3 grid((unsigned)((size_t)B * nblk));
-  if (bf16) {
-    prob_pass_kernel<bf16_t><<<grid, dim3(kProbPassThreads), 0, stream>>>(a, nblk);
-    prob_draw_kernel<bf16_t><<<dim3(B), dim3(kWave), 0, stream>>>(a);
-  } else {
-    prob_pass_kernel<float><<<grid, dim3(kProbPassThreads), 0, stream>>>(a, nblk);
-    prob_draw_kernel<float><<<dim3(B), dim3(kWave), 0, stream>>>(a);
-  }
+  if (bf16) prob_pass_kernel<bf16_t><<<grid, dim3(kProbPassThreads), 0, stream>>>(a, nblk);
+  else prob_pass_kernel<float><<<grid, dim3(kProbPassThreads), 0, stream>>>(a, nblk);
+  const bool held = a.nch <= kProbHeld * kProbBatch;
+  auto draw = bf16 ? held ? prob_draw_kernel<bf16_t, true> : prob_draw_kernel<bf16_t, false>
+                   : held ? prob_draw_kernel<float, true> : prob_draw_kernel<float, false>;
+  draw<<<dim3(B), dim3(kWave), 0, stream>>>(a);
   return hipGetLastError();
 }
 
