@@ -15,9 +15,9 @@
 // float32 residual (4.6 TB/s; a large copy reaches 4.9).  The narrow types are
 // bound by their instructions as much as by memory: packed conversions, one
 // reciprocal root and DPP sums took it from 37.9 us.  Workgroups that stay and
-// fetch the next row ahead gave 37.9 -> 35.8 us before that, but 46 -> 57 us with a float32
-// residual (registers), loads past the caches 33.0 -> 30.3 but 13.7 -> 14.9 us at
-// 1024 x 8192, where the rows still lie in them.
+// fetch the next row ahead gave 37.9 -> 35.8 us before that, but 46 -> 57 us with
+// a float32 residual (registers), loads past the caches 33.0 -> 30.3 but 13.7 ->
+// 14.9 us at 1024 x 8192, where the rows still lie in them.
 //
 // y is formed from r' before r' is rounded to its own type: one rounding less
 // between the residual stream and the logits.
@@ -50,21 +50,20 @@ struct NormArgs {
 // -> 4.6 us at 37 x 2047 float32 against 8 neighbours).
 enum NormLayout { kWide, kNeighbours, kApart };
 
-// Values e0, e0 + es, .. of a row as floats; those at or past D read as 0.
+// Values e0, e0 + es, .. of a row as floats; those at or past D read as 0.  No
+// branches: the row's arrays are all fetched before the first is waited for.
 template <typename T, int LAYOUT>
 __device__ __forceinline__ void norm_load(const T* row, int e0, int es, int D, float* v) {
-  if constexpr (LAYOUT == kWide) {
-    if (e0 < D) {                                        // D is a multiple of 8
+  if constexpr (LAYOUT == kWide) {                       // D is a multiple of 8
+    const int e = min(e0, D - 8);
 #pragma unroll
-      for (int i = 0; i < 8; i += Elem<T>::kPerVec) load_vec_fast(row, e0 + i, v + i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
+    for (int i = 0; i < 8; i += Elem<T>::kPerVec) load_vec_fast(row, e + i, v + i);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = e0 + i * es < D ? to_f32(row[e0 + i * es]) : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(row[min(e0 + i * es, D - 1)]);
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = e0 + i * es < D ? v[i] : 0.f;
 }
 
 // The same for a weight row of either type (uniform over the grid).
