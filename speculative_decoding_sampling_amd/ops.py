@@ -9,7 +9,7 @@ workspaces allocated with torch and raw device pointers and the HIP stream
 passed through the C ABI declared in ``include/specverify_ops.h``; here a native
 module (``csrc/ops_ext.cpp``) does so, since these operators are often shorter
 than the marshalling of a ctypes call.  If the libraries are not built the
-calls raise: there is no fallback.
+calls raise: there is no fallback.  Nothing here records gradients.
 
 8-bit values are ``torch.float8_e4m3fn`` tensors [..., D] with a
 ``torch.float8_e8m0fnu`` scale [..., D / 128] for each run of 128.
