@@ -11,13 +11,14 @@
 // workgroups on a compute unit.  The sums of squares are float32: per thread
 // in order, then the wave and the waves' sums on DPP moves, a fixed order.
 //
-// 2304 x 8192: 33.0 us from bfloat16 to 8-bit values (4.0 TB/s), 44.7 us with a
-// float32 residual (4.6 TB/s; a large copy reaches 4.9).  The narrow types are
+// 2304 x 8192: 30.2 us from bfloat16 to 8-bit values (4.4 TB/s), 44.6 us with a
+// float32 residual (4.7 TB/s; a large copy reaches 4.9).  The narrow types are
 // bound by their instructions as much as by memory: packed conversions, one
-// reciprocal root and DPP sums took it from 37.9 us.  Workgroups that stay and
-// fetch the next row ahead gave 37.9 -> 35.8 us before that, but 46 -> 57 us with
-// a float32 residual (registers), loads past the caches 33.0 -> 30.3 but 13.7 ->
-// 14.9 us at 1024 x 8192, where the rows still lie in them.
+// reciprocal root and DPP sums took the first from 37.9 to 33.0 us.  Workgroups
+// that stay and fetch the next row ahead gained 6 % there before that and lost
+// 24 % with a float32 residual (registers); loads past the caches gained 8 % there
+// and lost 9 % at 1024 x 8192, where the rows still lie in them; weights fetched
+// before the first reduction gained 6 % at 320 x 4096 and lost 11 % at 2304 x 8192.
 //
 // y is formed from r' before r' is rounded to its own type: one rounding less
 // between the residual stream and the logits.
@@ -51,7 +52,7 @@ struct NormArgs {
 enum NormLayout { kWide, kNeighbours, kApart };
 
 // Values e0, e0 + es, .. of a row as floats; those at or past D read as 0.  No
-// branches: the row's arrays are all fetched before the first is waited for.
+// branches: each would make the loads behind it wait for those before it.
 template <typename T, int LAYOUT>
 __device__ __forceinline__ void norm_load(const T* row, int e0, int es, int D, float* v) {
   if constexpr (LAYOUT == kWide) {                       // D is a multiple of 8
@@ -153,18 +154,25 @@ __global__ __launch_bounds__(kNormMaxThreads) void hidden_norm_kernel(NormArgs a
   for (int j = 0; j < NV; ++j) {
     const int e0 = at(j);
     norm_load<X, LAYOUT>(x, e0, es, D, h[j]);
-    if constexpr (kEarly) norm_load<R, LAYOUT>(r, e0, es, D, res[j]);
   }
-  float f = a.scale;
+  float f = a.scale, ss = 0.f;
   if (a.w1) {
-    float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
-    f = a.scale * inv_root(fmaf(block_sum(ss, red[0]), a.inv_d, a.eps));
   }
-  float ss = 0.f;
+  // The residual is fetched while the first reduction runs: before it, its
+  // reads delay those that the reduction waits for (2304 x 8192 bfloat16 to 8
+  // bits 32.2 -> 30.2 us, 320 x 4096 with a float32 residual 6.0 -> 5.6 us).
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (kEarly) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) norm_load<R, LAYOUT>(r, at(j), es, D, res[j]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  if (a.w1) f = a.scale * inv_root(fmaf(block_sum(ss, red[0]), a.inv_d, a.eps));
+  ss = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e0 = at(j);
