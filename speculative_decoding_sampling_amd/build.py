@@ -82,7 +82,7 @@ def _ext_commands():
                 *[f"-isystem{d}" for d in inc], "-c", os.path.join(CSRC, OPS_EXT_SOURCE),
                 "-o", _object(OPS_EXT_SOURCE)]
     link = [cxx, "-shared", "-o", OPS_EXT + ".tmp", _object(OPS_EXT_SOURCE), "-L", HERE,
-            "-lspecverify_ops", "-lspecverify", "-L", torch_lib, "-lc10", "-ltorch_cpu",
+            "-lspecverify_ops", "-lspecverify", "-L", torch_lib, "-lc10", "-ltorch_cpu", "-ltorch_hip",
             "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     return compile_, link
 

@@ -134,3 +134,13 @@ def test_path_of_the_small_batch_follows_other_work():
         ws = torch.full((n,), fill, device=DEV, dtype=torch.uint8)
         for _ in range(3):
             assert same(one_round(*ins, workspace=ws), want)
+
+
+def test_outputs_in_inference_mode():
+    x, w = torch.randn(4, 256, device=DEV), torch.ones(256, device=DEV)
+    want = S.hidden_norm(x, x, w)
+    with torch.inference_mode():
+        got = S.hidden_norm(x, x, w)
+        assert all(t.is_inference() for t in got) and same(got, want)
+    p = x.clone().requires_grad_(True)                            # no gradients are recorded
+    assert not any(t.requires_grad for t in S.hidden_norm(p, p, w))
