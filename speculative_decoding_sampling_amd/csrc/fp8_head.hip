@@ -520,9 +520,11 @@ __device__ __forceinline__ void fp8_tile(uint8_t* lds, uint32_t (&lsc)[2][kF8Thr
     }
 }
 
-// The last row block is a tile of the 32-row steps that it has (bfloat16, us: 320
-// x 128256 x 4096 219 -> 212, 200 rows 156 -> 150, 160 x 64000 x 4096 75 -> 66
-// against whole tiles).
+// The row blocks share the 32-row steps evenly, at most MT each: as many rows
+// as there are, and blocks that share weights keep in step, so that more of them
+// are found in L2.  bfloat16, us, against whole tiles / a short last block: 320 x
+// 128256 x 4096 219 / 213 -> 206, 257 rows 203 / 204 -> 186, 200 rows 156 / 150 ->
+// 149, 160 x 64000 x 4096 75 / 66 -> 65; float32 97 x 128256 x 4096 205 / 195 -> 176.
 template <int MT, bool ONCE, typename O>
 __global__ __launch_bounds__(kF8Threads, 2) void fp8_tile_kernel(
     const uint8_t* __restrict__ H, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ P,
@@ -533,8 +535,9 @@ __global__ __launch_bounds__(kF8Threads, 2) void fp8_tile_kernel(
   const int per = (nwork + kXcds - 1) / kXcds;
   const int work = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
   if (work >= nwork) return;                                 // blockIdx.x / kXcds < per
-  const int tile = work / nrb, m0 = (work % nrb) * 32 * MT;
-  const int steps = (M - m0 + 31) / 32;
+  const int tile = work / nrb, rb = work % nrb, all = (M + 31) / 32;
+  const int m0 = 32 * (rb * (all / nrb) + min(rb, all % nrb));
+  const int steps = all / nrb + (rb < all % nrb ? 1 : 0);
   if (MT > 3 && steps == 3)
     fp8_tile<MT < 3 ? MT : 3, ONCE>(lds, lsc, H, hs, P, ws, M, D, V, ngroup, tile, m0, out);
   else if (MT > 2 && steps == 2)
@@ -594,8 +597,8 @@ int fp8_choice(int M, int D, int V, bool exact) {
     const int nrb = (M + 32 * mt - 1) / (32 * mt);
     const double cus = tiles * nrb / 256;
     const double load = cus <= 1 ? 1 : cus <= 1.55 ? 1.55 : cus < 3 ? 1.12 * cus : cus;
-    const int last = (M - 32 * mt * (nrb - 1) + 31) / 32;      // 32-row steps of the last block
-    const double mean = ((nrb - 1) * run_ns[mt] + run_ns[last]) / nrb;
+    const int steps = (M + 31) / 32, low = steps / nrb, more = steps % nrb;
+    const double mean = (more * run_ns[more ? low + 1 : low] + (nrb - more) * run_ns[low]) / nrb;
     const double work = load * runs * mean * (exact ? 1.6 : 1);
     double rate = nrb == 1 ? 5400 : 4300;
     if (rate > 34 * tiles * nrb) rate = 34 * tiles * nrb;
