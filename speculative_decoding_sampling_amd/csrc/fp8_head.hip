@@ -576,33 +576,36 @@ hipError_t fp8_skinny(const Fp8Args& a, O* out) {
 
 constexpr double kFp8CacheBytes = 256.0 * (1 << 20);
 
-// Which product: 0 the skinny one, MT = 1..4 tiles of 32 MT hidden rows, by an
-// estimate of each one's time in nanoseconds, fitted to bfloat16 logits from
-// 1 x 128256 x 4096 to 1152 x 152064 x 4096 and down to 32 x 4000 x 512.
-//  - The skinny product reads the weights once for every 32 rows: 5.6 TB/s (4.3
-//    from memory with more than 16 rows, where the hidden rows' reads tell),
-//    6.5 for the blocks after the first.
+// Which product: 0 the skinny one, MT = 1..4 row blocks of at most 32 MT hidden
+// rows, by an estimate of each one's time in nanoseconds.  Its constants are
+// rates measured from 1 x 128256 x 4096 to 1152 x 152064 x 4096, start-up times
+// fitted over 517 random sizes (1 to 1152 rows, 1000 to 150000 ids, D from 128
+// to 8192, both logit types): the choice takes 1.6 % more than the best product
+// on average.
+//  - The skinny product reads the weights once for every 32 rows: 6.5 TB/s (4.3
+//    from memory with more than 16 rows, where the hidden rows' reads tell), 5.8
+//    for the blocks after the first.
 //  - A tile takes 0.65 to 1.06 us a run, two on a CU as long as one after the
-//    other; a little more than one to a CU on average is two on some.  All of
-//    them take at least the weights' time, 34 GB/s to a busy CU and 5.4 TB/s,
-//    4.3 where more than one row block reads them.
+//    other, one alone 0.7 of that; a little more than one to a CU on average is
+//    two on some.  All of them take at least the weights' time, 34 GB/s to a busy
+//    CU and 5.4 TB/s, 4.3 where more than one row block reads them.
 int fp8_choice(int M, int D, int V, bool exact) {
   const double bytes = (double)V * D, runs = D / kFp8Block;
   const double tiles = (V + kTileVocab - 1) / kTileVocab;
-  const double first = M > 16 && bytes > kFp8CacheBytes ? 4300 : 5600;
-  double best = 3500 + bytes / first + ((M + 31) / 32 - 1) * bytes / 6500;
+  const double first = M > 16 && bytes > kFp8CacheBytes ? 4300 : 6500;
+  double best = 2000 + bytes / first + ((M + 31) / 32 - 1) * bytes / 5800;
   int choice = 0;
   const double run_ns[5] = {0, 650, 730, 870, 1060};
   for (int mt = 1; mt <= (exact ? 3 : 4); ++mt) {
     const int nrb = (M + 32 * mt - 1) / (32 * mt);
     const double cus = tiles * nrb / 256;
-    const double load = cus <= 1 ? 1 : cus <= 1.55 ? 1.55 : cus < 3 ? 1.12 * cus : cus;
+    const double load = cus <= 1 ? 0.7 : cus <= 1.55 ? 1.55 : cus < 3 ? 1.12 * cus : cus;
     const int steps = (M + 31) / 32, low = steps / nrb, more = steps % nrb;
     const double mean = (more * run_ns[more ? low + 1 : low] + (nrb - more) * run_ns[low]) / nrb;
     const double work = load * runs * mean * (exact ? 1.6 : 1);
     double rate = nrb == 1 ? 5400 : 4300;
     if (rate > 34 * tiles * nrb) rate = 34 * tiles * nrb;
-    const double t = 3000 + (work > bytes / rate ? work : bytes / rate);
+    const double t = 6000 + (work > bytes / rate ? work : bytes / rate);
     if (t < best) {
       best = t;
       choice = mt;

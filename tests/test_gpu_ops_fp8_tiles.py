@@ -43,6 +43,9 @@ TILES = [
     (97, 33000, 640), (97, 60007, 2048), (120, 100003, 256), (128, 40960, 896), (128, 20001, 384),
     (129, 40960, 640), (200, 20001, 128), (257, 20001, 1024), (257, 33000, 1152), (300, 40960, 256),
     (385, 60007, 384), (520, 20001, 1152),
+    (65, 20001, 896), (33, 20001, 2944), (96, 20001, 1536), (50, 30720, 1536), (90, 20001, 4096),
+    (130, 20001, 896), (65, 32000, 896), (33, 40003, 1536), (96, 32000, 2048), (50, 50000, 2944),
+    (190, 30720, 1152), (250, 20001, 2048),
 ]
 
 
