@@ -357,7 +357,13 @@ __device__ __forceinline__ int prob_pick(const ProbArgs& a, int b, int lane, con
   return prob_draw<T>(rows, c, lane, a.V, before, t);
 }
 
-// Chunk sums: one wave per (request, chunk).
+// Chunk sums: one wave per (request, chunk).  Bound by memory where there is
+// enough of it: 31 us for the 156 MB of 256 x 8 x 152064 float32 without draft rows
+// (5.0 TB/s), 12.0 us at 64 x 4 x 128256 float32 (52 MB, 4.3 TB/s) and 8.9 us at 64 x
+// 8 x 129279 bfloat16 (33 MB), of which the scan's two dependent round trips before
+// the rows are some 3 us.  Registers allow seven waves a SIMD; eight spill (15.9 us
+// instead of 12.0), chunks of 2048 leave too few waves (21.9 us instead of 18.8 for
+// this kernel and the draw).
 template <typename T>
 __global__ __launch_bounds__(kProbPassThreads) void prob_pass_kernel(ProbArgs a, int nblk) {
   const int b = blockIdx.x / nblk;
@@ -376,9 +382,11 @@ __global__ __launch_bounds__(kProbPassThreads) void prob_pass_kernel(ProbArgs a,
   }
 }
 
-// The draws: one wave per request.  HELD: up to four batches of records are
-// fetched at once, beside the plan, and kept in registers for both walks.  (Four
-// variables: an array that is indexed at run time leaves the registers.)
+// The draws: one wave per request, a chain of round trips (records, the chunk).
+// HELD: up to four batches of records are fetched at once, beside the plan, and
+// kept in registers for both walks: 4.7 -> 4.2 us at 64 x 8 x 129279 bfloat16, 4.2 ->
+// 3.9 us at 64 x 4 x 128256 float32.  (Four variables: an array that is indexed at
+// run time leaves the registers, 8.7 us.)
 constexpr int kProbHeld = 4;
 template <typename T, bool HELD>
 __global__ __launch_bounds__(kWave) void prob_draw_kernel(ProbArgs a) {
@@ -416,7 +424,8 @@ __global__ __launch_bounds__(kWave) void prob_draw_kernel(ProbArgs a) {
   }
 }
 
-// Both in one workgroup per request.
+// Both in one workgroup per request: 7 us at 1 x 5 x 32000 float32, five dependent
+// round trips; two chunks in flight a wave change nothing (6.8 us).
 template <typename T>
 __global__ __launch_bounds__(kProbOneThreads) void prob_one_kernel(ProbArgs a) {
   __shared__ double recs[kProbOneChunks];
