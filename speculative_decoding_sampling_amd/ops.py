@@ -266,8 +266,10 @@ def verify_probs(target_probs, draft_probs, draft_tokens, draft_len, u, u_final,
     ``residual_mass``, ``stop_pos`` and ``path`` when ``debug`` is true, all as
     ``binding.verify`` gives them.  Asynchronous on ``stream``."""
     raw = _raw_stream(target_probs, stream)
-    if raw and stream is not None and workspace is None and target_probs.dim() == 3:
-        # allocated on the stream that uses it: it is given back right after
+    if stream is not None and workspace is None and isinstance(target_probs, torch.Tensor) and \
+            target_probs.is_cuda and target_probs.dim() == 3:
+        # allocated on the stream that uses it, the default stream (raw handle
+        # 0) as well: it is given back right after
         B, K1, V = target_probs.shape
         with torch.cuda.stream(stream):
             workspace = torch.empty(verify_probs_workspace_bytes(B, K1 - 1, V), dtype=torch.uint8,
