@@ -234,8 +234,10 @@ __device__ __forceinline__ int prob_lane(double incl, double term, double t) {
 }
 
 // The token of chunk c at t, base being the weights before the chunk: the
-// first whose running sum exceeds t, or where rounding leaves none the last
-// with a positive weight.
+// first with a positive weight whose running sum exceeds t, or where rounding
+// leaves none the last with one.  The weight is looked at because the scans
+// add in an order of each lane's own: base and the sum before a lane may be a
+// rounding above that of the last lane with weight, and so above t already.
 template <typename T>
 __device__ __forceinline__ int prob_draw(const ProbRows<T>& r, int c, int lane, int V, double base,
                                          double t) {
@@ -256,7 +258,7 @@ __device__ __forceinline__ int prob_draw(const ProbRows<T>& r, int c, int lane, 
   for (int i = 0; i < kProbPer; ++i) {
     const double w = prob_weight(p[i], q[i]);
     run += w;
-    if (first == kProbPer && run > t) first = i;
+    if (first == kProbPer && w > 0.0 && run > t) first = i;
     if (w > 0.0) last = i;
   }
   const int L = prob_lane(base + incl, sum, t) & (kWave - 1);
