@@ -150,10 +150,11 @@ SPECV_OPS_API specv_status_t specv_fp8_lm_head(const uint8_t *hidden, const uint
  * target_logits [B][K+1][V] bfloat16 from hidden [B][K+1][D], and
  * specv_verify_debug runs on them, with the same arguments, status codes,
  * per-request errors and nullable diagnostics.  The workspace is at least
- * specv_verify_fp8_lm_head_workspace_bytes(...) bytes, 16-byte aligned.  In a
- * captured graph that takes path 3 (specv_path_kind) it either belongs to
- * that graph alone, untouched between replays, or is cleared by a fill kernel
- * in the graph before this call.
+ * specv_verify_fp8_lm_head_workspace_bytes(...) bytes, 16-byte aligned.
+ * Outputs and workspace do not overlap the inputs or each other.  In a
+ * captured graph that takes path 3 (specv_path_kind) the workspace either
+ * belongs to that graph alone, untouched between replays, or is cleared by a
+ * fill kernel in the graph before this call.
  */
 SPECV_OPS_API size_t specv_verify_fp8_lm_head_workspace_bytes(int B, int K, int V, int D, int top_k,
                                                               float top_p);

@@ -38,15 +38,27 @@ bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 bool known(specv_dtype_t t) { return t == SPECV_F32 || t == SPECV_BF16; }
 size_t size_of(specv_dtype_t t) { return t == SPECV_BF16 ? 2 : 4; }
 
-// An array by its bytes (null: none).
+// An array by its bytes (null or empty: none).
 struct Span {
   const void* p;
   size_t n;
 };
 bool overlap(const Span& a, const Span& b) {
-  if (!a.p || !b.p) return false;
+  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
   return x < y + b.n && y < x + a.n;
+}
+
+// Whether an output lies over an input or over another output.
+template <size_t NO, size_t NI>
+bool clash(const Span (&out)[NO], const Span (&in)[NI]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (size_t j = 0; j < NI; ++j)
+      if (overlap(out[i], in[j])) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return true;
+  }
+  return false;
 }
 
 specv_status_t status(hipError_t e) { return e == hipSuccess ? SPECV_OK : SPECV_EHIP; }
@@ -200,6 +212,17 @@ specv_status_t specv_verify_fp8_lm_head(
   const size_t need = specv_workspace_bytes(B, K, V, SPECV_BF16, top_k, top_p);
   if (need == 0) return SPECV_EUNSUPPORTED;
   if (!workspace || misaligned(workspace, 16) || workspace_bytes < need) return SPECV_EWORKSPACE;
+  // the logits are written before the verification reads its inputs
+  const size_t rows = (size_t)B * (K + 1), nk = (size_t)B * K;
+  const Span in[8] = {{hidden, rows * D}, {hidden_scale, rows * D / SPECV_FP8_BLOCK},
+                      {packed_weight, fp8_packed_bytes(V, D)}, {draft_logits, nk * V * 2},
+                      {draft_tokens, nk * 4}, {draft_len, (size_t)B * 4}, {u, nk * 4},
+                      {u_final, (size_t)B * 4}};
+  const Span o[8] = {{target_logits, rows * V * 2}, {out_tokens, rows * 4},
+                     {n_emitted, (size_t)B * 4}, {accept_prob, nk * 4},
+                     {residual_mass, (size_t)B * 8}, {stop_pos, (size_t)B * 4},
+                     {path, (size_t)B * 4}, {workspace, need}};
+  if (clash(o, in)) return SPECV_EINVAL;
   const specv_status_t head = specv_fp8_lm_head(hidden, hidden_scale, packed_weight, B * (K + 1), D,
                                                 V, target_logits, SPECV_BF16, stream);
   if (head != SPECV_OK) return head;
@@ -247,17 +270,12 @@ specv_status_t specv_verify_probs(const void* target_probs, int64_t target_strid
   if (need > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
     return SPECV_EWORKSPACE;
   // the waves of a request read its inputs while one of them writes its outputs
-  const Span in[4] = {{K > 0 ? draft_tokens : nullptr, nk * 4}, {draft_len, (size_t)B * 4},
-                      {K > 0 ? u : nullptr, nk * 4}, {u_final, (size_t)B * 4}};
+  const Span in[4] = {{draft_tokens, nk * 4}, {draft_len, (size_t)B * 4}, {u, nk * 4},
+                      {u_final, (size_t)B * 4}};
   const Span o[7] = {{out_tokens, (nk + B) * 4}, {n_emitted, (size_t)B * 4}, {accept_prob, nk * 4},
                      {residual_mass, (size_t)B * 8}, {stop_pos, (size_t)B * 4},
-                     {path, (size_t)B * 4}, {need > 0 ? workspace : nullptr, need}};
-  for (int i = 0; i < 7; ++i) {
-    for (int j = 0; j < 4; ++j)
-      if (overlap(o[i], in[j])) return SPECV_EINVAL;
-    for (int j = 0; j < i; ++j)
-      if (overlap(o[i], o[j])) return SPECV_EINVAL;
-  }
+                     {path, (size_t)B * 4}, {workspace, need}};
+  if (clash(o, in)) return SPECV_EINVAL;
   return status(launch_verify_probs(dtype == SPECV_BF16, target_probs, target_stride_b,
                                     target_stride_k, draft_probs, draft_stride_b, draft_stride_k,
                                     draft_tokens, draft_len, u, u_final, B, K, V, eos_id,
