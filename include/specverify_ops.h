@@ -195,7 +195,8 @@ SPECV_OPS_API specv_status_t specv_verify_fp8_lm_head(
  *  accept_prob, residual_mass, stop_pos, path: nullable diagnostics, as for
  *                specv_verify_debug.
  *
- * Outputs and workspace do not overlap the inputs or each other.
+ * Outputs and workspace do not overlap the inputs or each other; between rows
+ * whose strides leave room they may lie.
  *
  * 1 <= B, 0 <= K <= SPECV_MAX_K, 1 <= V <= SPECV_MAX_V.  Per-request errors
  * as specv_verify (draft_len, a token or a uniform out of range, q(x) not

@@ -49,6 +49,33 @@ bool overlap(const Span& a, const Span& b) {
   return x < y + b.n && y < x + a.n;
 }
 
+// The rows of a probability tensor: nk for each of B requests, n bytes each,
+// at strides of sb and sk bytes (null: none).
+struct Rows {
+  const void* p;
+  size_t sb, sk;
+  int B, nk;
+  size_t n;
+};
+// Whether an array lies over one of the rows (between them it may lie).  Few
+// calls get past the first comparison.
+bool overlaps_rows(const Span& a, const Rows& r) {
+  if (!r.p || r.nk == 0) return false;
+  const size_t last = (size_t)(r.B - 1) * r.sb + (size_t)(r.nk - 1) * r.sk;
+  if (!overlap(a, Span{r.p, last + r.n})) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(r.p);
+  for (int b = 0; b < r.B; ++b) {
+    const uintptr_t first = y + (size_t)b * r.sb;
+    size_t k = 0;                                  // the request's first row that ends past x
+    if (x >= first + r.n) {
+      if (r.sk == 0) continue;
+      k = (x - first - r.n) / r.sk + 1;
+    }
+    if (k < (size_t)r.nk && first + k * r.sk < x + a.n) return true;
+  }
+  return false;
+}
+
 // Whether an output lies over an input or over another output.
 template <size_t NO, size_t NI>
 bool clash(const Span (&out)[NO], const Span (&in)[NI]) {
@@ -276,6 +303,10 @@ specv_status_t specv_verify_probs(const void* target_probs, int64_t target_strid
                      {residual_mass, (size_t)B * 8}, {stop_pos, (size_t)B * 4},
                      {path, (size_t)B * 4}, {workspace, need}};
   if (clash(o, in)) return SPECV_EINVAL;
+  const Rows t = {target_probs, target_stride_b * esz, target_stride_k * esz, B, K + 1, V * esz};
+  const Rows d = {draft_probs, draft_stride_b * esz, draft_stride_k * esz, B, K, V * esz};
+  for (const Span& s : o)
+    if (overlaps_rows(s, t) || overlaps_rows(s, d)) return SPECV_EINVAL;
   return status(launch_verify_probs(dtype == SPECV_BF16, target_probs, target_stride_b,
                                     target_stride_k, draft_probs, draft_stride_b, draft_stride_k,
                                     draft_tokens, draft_len, u, u_final, B, K, V, eos_id,
