@@ -27,9 +27,10 @@ from .binding import SpecVerifyError
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspecverify_ops.so")
 
 FP8_BLOCK = 128
-E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+# None in a torch without the type: the package's other calls do without it
+E4M3, E8M0 = getattr(torch, "float8_e4m3fn", None), getattr(torch, "float8_e8m0fnu", None)
 _VALUE_CODES = {torch.float32: 0, torch.bfloat16: 1}
-_OUT_CODES = {**_VALUE_CODES, E4M3: 2}
+_OUT_CODES = {**_VALUE_CODES, **({E4M3: 2} if E4M3 else {})}
 
 _lib = None
 _native = None
