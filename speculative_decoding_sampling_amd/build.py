@@ -87,19 +87,36 @@ def _ext_commands():
     return compile_, link
 
 
+def _build_ext():
+    ext_compile, ext_link = _ext_commands()
+    return _run(ext_compile), ext_link
+
+
 def build(verbose=False):
+    """Compile everything and link it in the order of what it needs: a library
+    is in place even if something after it does not build, which is then raised."""
     hipcc = _hipcc()
     os.makedirs(BUILD, exist_ok=True)
-    ext_compile, ext_link = _ext_commands()
-    cmds = [[hipcc, *FLAGS, "-c", os.path.join(CSRC, src), "-o", _object(src)]
-            for src in SOURCES + OPS_SOURCES] + [ext_compile]
-    with ThreadPoolExecutor(max_workers=min(len(cmds), os.cpu_count() or 1, 8)) as ex:
-        outs = list(ex.map(_run, cmds))
-    outs.append(_link(hipcc, LIB, SOURCES))
-    outs.append(_link(hipcc, OPS_LIB, OPS_SOURCES, "-L", HERE, "-lspecverify",
-                      "-Wl,-rpath,$ORIGIN"))
-    outs.append(_run(ext_link))
-    os.replace(OPS_EXT + ".tmp", OPS_EXT)
+    sources = SOURCES + OPS_SOURCES
+    with ThreadPoolExecutor(max_workers=min(len(sources) + 1, os.cpu_count() or 1, 8)) as ex:
+        objects = [ex.submit(_run, [hipcc, *FLAGS, "-c", os.path.join(CSRC, src), "-o", _object(src)])
+                   for src in sources]
+        # the only step that needs g++ and torch's headers
+        module = ex.submit(_build_ext)
+        outs = [f.result() for f in objects[:len(SOURCES)]]
+        outs.append(_link(hipcc, LIB, SOURCES))
+        outs += [f.result() for f in objects[len(SOURCES):]]
+        outs.append(_link(hipcc, OPS_LIB, OPS_SOURCES, "-L", HERE, "-lspecverify",
+                          "-Wl,-rpath,$ORIGIN"))
+    try:
+        out, ext_link = module.result()
+        outs += [out, _run(ext_link)]
+        os.replace(OPS_EXT + ".tmp", OPS_EXT)
+    except BaseException:
+        # an older module may not fit the new library
+        if os.path.exists(OPS_EXT):
+            os.remove(OPS_EXT)
+        raise
     if verbose:
         for o in outs:
             if o.strip():
