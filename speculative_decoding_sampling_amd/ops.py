@@ -197,7 +197,9 @@ def _packed(packed):
 def fp8_lm_head(hidden, hidden_scale, packed, *, dtype=torch.bfloat16, logits=None, stream=None):
     """Logits [..., V] (``dtype`` bf16 or fp32) of hidden states [..., D]
     float8_e4m3fn with their scales (``hidden_norm`` or ``quantize_fp8``) and a
-    ``PackedFp8LmHead``; float32 accumulation.  Asynchronous on ``stream``."""
+    ``PackedFp8LmHead``.  fp32 logits accumulate in float32; bf16 logits take the
+    8-bit matrix product, whose sums hold fewer bits: up to 2^-10 of sum |h w|
+    off before their rounding.  Asynchronous on ``stream``."""
     logits, = _done((_native or _load_native()).fp8_lm_head(
         hidden, hidden_scale, *_packed(packed), _value_code(dtype), logits,
         _raw_stream(hidden, stream)), stream)
