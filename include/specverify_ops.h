@@ -132,7 +132,7 @@ SPECV_OPS_API specv_status_t specv_fp8_lm_head_pack_weight(const uint8_t *q, con
  * each 8 products that it adds at once it drops of each what lies below 2^-13
  * of the largest, before it adds them to a float32 sum.  Besides the rounding a
  * bfloat16 logit may so be off by up to 2^-10 of sum |h w| (on random operands
- * some 1e-5 to 6e-5 of a typical logit, 0.4 to 1.6 % of 2^-8: one logit in 60
+ * some 1e-5 to 6e-5 of a typical logit, 0.3 to 1.5 % of 2^-8: one logit in 60
  * rounds the other way), which tells where large products cancel.
  *
  *  hidden         [M][D] e4m3 bytes, 16-byte aligned.

@@ -19,6 +19,10 @@
 // 24 % with a float32 residual (registers); loads past the caches gained 8 % there
 // and lost 9 % at 1024 x 8192, where the rows still lie in them; weights fetched
 // before the first reduction gained 6 % at 320 x 4096 and lost 11 % at 2304 x 8192.
+// Rows of other than whole 8s, element by element: 2304 x 8191 bfloat16 36.8 us
+// (4.1 TB/s).  Past 16384 values every row takes the kernel of eight groups a
+// thread, those past its end masked: 1152 x 16384 bfloat16 32.5 us (4.6 TB/s),
+// 16392 63 us, 32768 86 us (3.5 TB/s), 576 x 65536 80 us (3.8 TB/s).
 //
 // y is formed from r' before r' is rounded to its own type: one rounding less
 // between the residual stream and the logits.

@@ -361,9 +361,10 @@ __device__ __forceinline__ int prob_pick(const ProbArgs& a, int b, int lane, con
 
 // Chunk sums: one wave per (request, chunk).  Bound by memory where there is
 // enough of it: 31 us for the 156 MB of 256 x 8 x 152064 float32 without draft rows
-// (5.0 TB/s), 12.0 us at 64 x 4 x 128256 float32 (52 MB, 4.3 TB/s) and 8.9 us at 64 x
-// 8 x 129279 bfloat16 (33 MB), of which the scan's two dependent round trips before
-// the rows are some 3 us.  Registers allow seven waves a SIMD; eight spill (15.9 us
+// (5.1 TB/s with what it reads twice; the fastest read of this card is 6.9), 12.2 us
+// at 64 x 4 x 128256 float32 (52 MB read, 4.3 TB/s) and 8.8 us at 64 x 8 x 129279
+// bfloat16 (26 MB read, 2.9 TB/s), of which the scan's two dependent round trips
+// before the rows are some 3 us.  Registers allow seven waves a SIMD; eight spill (15.9 us
 // instead of 12.0), chunks of 2048 leave too few waves (21.9 us instead of 18.8 for
 // this kernel and the draw).
 template <typename T>
