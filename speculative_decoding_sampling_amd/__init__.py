@@ -12,6 +12,12 @@ the operators around that step: ``verify_probs`` (the verification from given
 probabilities), ``hidden_norm`` (the norms before the LM head) and the LM head
 on 8-bit floats (``quantize_fp8``, ``pack_fp8_lm_head``, ``fp8_lm_head``,
 ``verify_fp8_lm_head``).
+
+``libspecverify_draft.so`` (``include/specverify_draft.h``, bound in ``draft``)
+holds the operators of a draft step: the LM head on 4-bit floats
+(``quantize_fp4``, ``pack_fp4_lm_head``, ``fp4_lm_head``) and distributions and
+draws after temperature, top-k, top-p and min-p with each request's own
+parameters (``filter_probs``, ``sample_filtered``).
 """
 
 from .binding import (  # noqa: F401
@@ -30,6 +36,16 @@ from .binding import (  # noqa: F401
     status_string,
     verify,
     workspace_bytes,
+)
+from .draft import (  # noqa: F401
+    PackedFp4LmHead,
+    draft_library_path,
+    filter_probs,
+    fp4_lm_head,
+    load_draft_library,
+    pack_fp4_lm_head,
+    quantize_fp4,
+    sample_filtered,
 )
 from .ops import (  # noqa: F401
     PackedFp8LmHead,

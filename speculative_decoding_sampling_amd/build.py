@@ -1,11 +1,14 @@
-"""Build libspecverify.so and libspecverify_ops.so in-tree with hipcc for gfx950.
+"""Build libspecverify.so, libspecverify_ops.so and libspecverify_draft.so in-tree
+with hipcc for gfx950.
 
 Usage: ``python -m speculative_decoding_sampling_amd.build`` (or
 ``__graft_entry__.build()``).  Compiles every source under ``csrc/`` to an
-object in ``_build/`` in parallel and links the two shared libraries next to
-this file, where the Python bindings load them.  libspecverify_ops calls
+object in ``_build/`` in parallel and links the shared libraries next to this
+file, where the Python bindings load them.  libspecverify_ops calls
 libspecverify's public entry points and finds it in its own folder; the Python
-module _ops_native (host C++, torch's headers) calls libspecverify_ops.
+modules _ops_native and _draft_native (host C++, torch's headers) call
+libspecverify_ops and libspecverify_draft.  ``build()`` makes the first two
+libraries and their module, ``build_draft()`` the third and its own.
 """
 
 import os
@@ -30,6 +33,10 @@ OPS_SOURCES = ["ops.hip", "probs.hip", "hidden_norm.hip", "fp8_head.hip"]
 # Python module of the operators, host C++ against torch's headers
 OPS_EXT = os.path.join(HERE, "_ops_native.so")
 OPS_EXT_SOURCE = "ops_ext.cpp"
+DRAFT_LIB = os.path.join(HERE, "libspecverify_draft.so")
+DRAFT_SOURCES = ["draft.hip", "fp4_head.hip", "filter_draw.hip"]
+DRAFT_EXT = os.path.join(HERE, "_draft_native.so")
+DRAFT_EXT_SOURCE = "draft_ext.cpp"
 # Packed FP32 instructions stay off: the compiler must not form v_pk_* FP32 ops.
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
@@ -66,8 +73,8 @@ def _link(hipcc, lib, sources, *extra):
     return out
 
 
-def _ext_commands():
-    """Compile and link command of the Python module."""
+def _ext_commands(source=OPS_EXT_SOURCE, libs=("-lspecverify_ops", "-lspecverify"), ext=None):
+    """Compile and link command of a Python module, the operators' by default."""
     import sysconfig
 
     import torch
@@ -79,10 +86,9 @@ def _ext_commands():
            *cpp_extension.include_paths()]
     compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
                 "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-                *[f"-isystem{d}" for d in inc], "-c", os.path.join(CSRC, OPS_EXT_SOURCE),
-                "-o", _object(OPS_EXT_SOURCE)]
-    link = [cxx, "-shared", "-o", OPS_EXT + ".tmp", _object(OPS_EXT_SOURCE), "-L", HERE,
-            "-lspecverify_ops", "-lspecverify", "-L", torch_lib, "-lc10", "-ltorch_cpu", "-ltorch_hip",
+                *[f"-isystem{d}" for d in inc], "-c", os.path.join(CSRC, source), "-o", _object(source)]
+    link = [cxx, "-shared", "-o", (ext or OPS_EXT) + ".tmp", _object(source), "-L", HERE, *libs,
+            "-L", torch_lib, "-lc10", "-ltorch_cpu", "-ltorch_hip",
             "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     return compile_, link
 
@@ -124,5 +130,37 @@ def build(verbose=False):
     return LIB
 
 
+def build_draft(verbose=False):
+    """The library of the draft step's operators and its Python module, in the
+    same order and with the same care."""
+    hipcc = _hipcc()
+    os.makedirs(BUILD, exist_ok=True)
+
+    def module():
+        compile_, link = _ext_commands(DRAFT_EXT_SOURCE, ("-lspecverify_draft",), DRAFT_EXT)
+        return _run(compile_), link
+
+    with ThreadPoolExecutor(max_workers=len(DRAFT_SOURCES) + 1) as ex:
+        objects = [ex.submit(_run, [hipcc, *FLAGS, "-c", os.path.join(CSRC, src), "-o", _object(src)])
+                   for src in DRAFT_SOURCES]
+        ext = ex.submit(module)
+        outs = [f.result() for f in objects]
+        outs.append(_link(hipcc, DRAFT_LIB, DRAFT_SOURCES))
+    try:
+        out, link = ext.result()
+        outs += [out, _run(link)]
+        os.replace(DRAFT_EXT + ".tmp", DRAFT_EXT)
+    except BaseException:
+        if os.path.exists(DRAFT_EXT):
+            os.remove(DRAFT_EXT)
+        raise
+    if verbose:
+        for o in outs:
+            if o.strip():
+                print(o)
+    return DRAFT_LIB
+
+
 if __name__ == "__main__":
     print(build(verbose="-v" in sys.argv))
+    print(build_draft(verbose="-v" in sys.argv))

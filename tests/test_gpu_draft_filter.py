@@ -1,0 +1,347 @@
+"""Filtered distributions and draws on the GPU against the fp64 reference.
+
+Tokens must equal the reference's draw unless its t lies within 1e-10 of the mass
+from another token, or a top-p or min-p decision within 1e-9 of the other
+outcome (n weights held to 2^-46 are off by n 2^-47 at most, 1e-9 at n = 150000).
+A probability is exp2(f) 2^k / S: the hardware's exp2 within 1 ulp (2^-23), f, a
+float32 in [-1/2, 1/2] rounded once (2^-26), the sum's reciprocal and the product
+(2^-24 each): below 2^-22 (1 + 1/8) of the value, and 2^-126 where it is subnormal;
+then half a step of the output type.
+"""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import speculative_decoding_sampling_amd as S  # noqa: E402
+from oracle import draft as OD  # noqa: E402
+from speculative_decoding_sampling_amd import binding, draft  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+REL = 2.0 ** -22 * 1.125
+
+
+def logits(R, V, seed, dtype=F32, spread=2.5, spikes=8):
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randn(R, V, generator=g) * spread
+    if spikes and V >= 4 * spikes:
+        at = torch.randint(0, V, (R, spikes), generator=g)
+        z.scatter_add_(1, at, torch.rand(R, spikes, generator=g) * 12)
+    return z.to(dtype)
+
+
+def per_row(v, i, L):
+    return v if not isinstance(v, torch.Tensor) else v[i // L].item()
+
+
+def check(z, u, T, k, p, mp, probs=None, tokens=None, L=1):
+    """Compares [R, V] probabilities and [R] tokens with the reference; returns
+    how many rows were too near a border to be compared."""
+    z = z.double().cpu().numpy()
+    near = 0
+    for i in range(len(z)):
+        P, margin = OD.filtered(z[i], *(per_row(x, i, L) for x in (T, k, p, mp)))
+        if margin < 1e-9:
+            near += 1
+            continue
+        if probs is not None:
+            got = probs[i].double().cpu().numpy()
+            if P is None:
+                assert (got == 0).all(), i
+            else:
+                eps = torch.finfo(probs.dtype).eps / 2
+                # P > 0 but below the smallest float may come out as 0
+                assert np.all((got > 0) <= (P > 0)) and np.all((P < 2.0 ** -120) | ((P > 0) == (got > 0))), i
+                tol = P * REL + 2.0 ** -126
+                assert np.all(np.abs(got - P) <= tol + (P + tol) * eps), \
+                    (i, np.max(np.abs(got - P) / np.maximum(P, 1e-30)))
+        if tokens is not None:
+            y, m = OD.draw(P, float(u[i]))
+            assert int(tokens[i]) == y or m < 1e-10, (i, int(tokens[i]), y, m)
+    return near
+
+
+def both(z, u, T=1.0, k=0, p=1.0, mp=0.0, dtype=F32):
+    """Tokens alone and with probabilities: the same call's two forms."""
+    zd = z.to(DEV)
+    args = tuple(x.to(DEV) if isinstance(x, torch.Tensor) else x for x in (T, k, p, mp))
+    tok = S.sample_filtered(zd, u.to(DEV), *args)
+    probs, tok2 = S.filter_probs(zd, *args, u=u.to(DEV), dtype=dtype)
+    assert torch.equal(tok, tok2)
+    assert torch.equal(probs, S.filter_probs(zd, *args, dtype=dtype))
+    return probs, tok
+
+
+FILTERS = [(1.0, 0, 1.0, 0.0), (0.7, 50, 1.0, 0.0), (1.3, 0, 0.9, 0.0), (0.9, 0, 1.0, 0.05),
+           (0.8, 40, 0.95, 0.02), (0.0, 0, 1.0, 0.0), (1.0, 1, 1.0, 0.0), (5.0, 300, 0.999, 0.0),
+           (0.01, 0, 0.5, 0.0), (1.0, 0, 0.00001, 1.0), (100.0, 0, 0.3, 0.0), (1.0, 3000, 0.9, 0.0)]
+
+
+@pytest.mark.parametrize("V", [1, 2, 3, 7, 64, 100, 1000, 4097, 32000])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_against_the_reference(V, dtype):
+    R = 6
+    near = 0
+    for n, (T, k, p, mp) in enumerate(FILTERS):
+        print(f"[filter] V={V} {dtype} T={T} k={k} p={p} mp={mp}", flush=True)
+        z = logits(R, V, 17 * n + V, dtype)
+        u = torch.rand(R, generator=torch.Generator().manual_seed(n))
+        probs, tok = both(z, u, T, k, p, mp, BF if n % 2 else F32)
+        near += check(z, u, T, k, p, mp, probs, tok)
+    assert near <= 1 + len(FILTERS) * R // 20
+
+
+@pytest.mark.parametrize("V,dtype,spread", [(128256, BF, 2.5), (152064, F32, 2.2), (129279, F32, 0.5),
+                                            (262147, BF, 3.0), (600000, F32, 2.0)])
+def test_long_rows_each_request_with_its_own_filters(V, dtype, spread):
+    print(f"[filter] V={V} {dtype}", flush=True)
+    T = torch.tensor([1.0, 0.0, 0.7, 1.2, 0.9, 0.8, 2.0])
+    k = torch.tensor([0, 0, 100, 0, 0, 64, 5000], dtype=I32)
+    p = torch.tensor([1.0, 1.0, 1.0, 0.95, 1.0, 0.9, 0.8])
+    mp = torch.tensor([0.0, 0.0, 0.0, 0.0, 0.03, 0.01, 0.0])
+    z = logits(7, V, V, dtype, spread, 40)
+    u = torch.rand(7, generator=torch.Generator().manual_seed(V))
+    probs, tok = both(z, u, T, k, p, mp)
+    assert check(z, u, T, k, p, mp, probs, tok) <= 1
+
+
+def test_largest_vocabulary():
+    V = 4194304
+    z = logits(3, V, 5, BF, 2.0, 40)
+    u = torch.tensor([0.3, 0.99999, 0.5])
+    T, k = torch.tensor([1.0, 0.8, 1.0]), torch.tensor([0, 0, 20000], dtype=I32)
+    p, mp = torch.tensor([1.0, 0.9, 0.9]), 0.0
+    probs, tok = both(z, u, T, k, p, mp)
+    assert check(z, u, T, k, p, mp, probs, tok) <= 1
+
+
+def test_uniforms_at_the_ends():
+    z = logits(4, 5000, 3)
+    z[1, :2500] = -np.inf
+    z[2, 2500:] = -np.inf
+    for u0 in (0.0, 1 - 2.0 ** -24, 2.0 ** -149):
+        u = torch.full((4,), u0)
+        for f in ((1.0, 0, 1.0, 0.0), (0.5, 20, 0.9, 0.0)):
+            probs, tok = both(z, u, *f)
+            check(z, u, *f, probs, tok)
+
+
+def test_masked_and_bad_rows():
+    V = 3000
+    z = logits(12, V, 8)
+    z[0, 1:] = -np.inf                                  # one token left
+    z[1] = -np.inf                                      # none
+    z[2, 77] = np.nan
+    z[3, 2999] = np.inf
+    z[4, 5:] = -np.inf
+    z[5] = -3.4028234663852886e38                       # the type's lowest value everywhere
+    z[6] = -3.4028234663852886e38
+    z[6, 100] = 0.0
+    z[7] = 3.4028234663852886e38
+    z[8] = 0.0
+    z[8, ::2] = -0.0                                    # equal to it
+    z[9] = 1e-40                                        # subnormal
+    z[9, 10] = 2e-40
+    z[10, 3] = -np.nan
+    u = torch.rand(12, generator=torch.Generator().manual_seed(1))
+    u[11] = 1.0
+    for f in ((1.0, 0, 1.0, 0.0), (0.7, 10, 1.0, 0.0), (1.0, 0, 0.9, 0.0), (1.0, 0, 1.0, 0.5), (0.0, 0, 1.0, 0.0),
+              (1.0, 7, 0.5, 0.1)):
+        tok = S.sample_filtered(z.to(DEV), u.to(DEV), *f)
+        probs = S.filter_probs(z.to(DEV), *f)
+        check(z, u, *f, probs, None)
+        check(z[:5], u, *f, None, tok)
+        assert tok[[1, 2, 3, 10, 11]].tolist() == [-1] * 5
+        assert float(probs[11].sum()) > 0.99            # u does not matter to the distribution
+        assert (S.filter_probs(z.to(DEV), *f, u=u.to(DEV))[0][11] == 0).all()
+        assert 0 <= int(tok[8]) < V and (int(tok[6]) == 100)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_ties_are_kept_together(dtype):
+    V = 4000
+    g = torch.Generator().manual_seed(2)
+    z = torch.randint(-4, 5, (8, V), generator=g).float().to(dtype)   # some 440 of each value
+    u = torch.rand(8, generator=g)
+    near = 0
+    for f in ((1.0, 5, 1.0, 0.0), (1.0, 500, 1.0, 0.0), (1.0, 0, 0.3, 0.0), (1.0, 0, 0.9, 0.0), (2.0, 900, 0.7, 0.2),
+              (0.0, 0, 1.0, 0.0)):
+        probs, tok = both(z, u, *f)
+        near += check(z, u, *f, probs, tok)
+    assert near == 0
+    # equal logits everywhere: all are kept
+    z = torch.full((2, V), 1.25, dtype=dtype)
+    for f in ((1.0, 3, 1.0, 0.0), (0.3, 0, 0.01, 1.0)):
+        probs, tok = both(z, u[:2], *f)
+        assert check(z, u, *f, probs, tok) == 0 and (probs > 0).all()
+
+
+def test_top_p_that_is_met_exactly():
+    # four equal weights of two values each way: 0.5 is reached by the first two
+    z = torch.full((3, 64), -np.inf)
+    z[:, [3, 9, 20, 40]] = torch.tensor([1.0, 1.0, 0.0, 0.0])
+    z[1, 3] = 0.0
+    z[2, [3, 9, 20, 40]] = 2.0
+    probs = S.filter_probs(z.to(DEV), 1e30, 0, 0.5)      # T so large that all weights are 1
+    # row 0: the two ones hold half; row 1: only one 1, then the zeros together
+    assert [(r > 0).nonzero()[:, 0].tolist() for r in probs.cpu()] == [[3, 9], [3, 9, 20, 40], [3, 9, 20, 40]]
+
+
+@pytest.mark.parametrize("L", [1, 3])
+@pytest.mark.parametrize("dtype,odtype", [(F32, F32), (BF, F32), (F32, BF), (BF, BF)])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (1, 1), (3, 2), (5, 7)])
+def test_strides_and_alignment(L, dtype, odtype, pad, shift):
+    B, V = 4, 1531
+    T, k = torch.tensor([1.0, 0.8, 0.0, 1.1]).to(DEV), torch.tensor([0, 30, 0, 0], dtype=I32).to(DEV)
+    p = torch.tensor([1.0, 1.0, 1.0, 0.8]).to(DEV)
+    src = torch.full((B, L, V + pad + shift), 99.0).to(dtype)
+    src[..., shift:shift + V] = logits(B * L, V, 4, dtype).reshape(B, L, V)
+    z = src.to(DEV)[..., shift:shift + V]
+    u = torch.rand(B, 2 * L, generator=torch.Generator().manual_seed(3)).to(DEV)[:, ::2]
+    out = torch.full((B, L + 2, V + pad + shift), 7.0, dtype=odtype, device=DEV)
+    tok = torch.full((L + 1, B), -7, dtype=I32, device=DEV)
+    po, to = out[:, 1:L + 1, shift:shift + V], tok[:L].t()
+    if L == 1:
+        z, u, po, to = z[:, 0], u[:, 0], po[:, 0], to[:, 0]
+    probs, t = S.filter_probs(z, T, k, p, u=u, dtype=odtype, probs=po, out_tokens=to)
+    assert probs.data_ptr() == po.data_ptr() and t.data_ptr() == to.data_ptr()
+    check(z.reshape(B * L, V), u.reshape(-1).cpu(), T.cpu(), k.cpu(), p.cpu(), 0.0, po.reshape(B * L, V),
+          to.reshape(-1), L)
+    # nothing around them is touched
+    assert (out[:, 0] == 7).all() and (out[:, L + 1] == 7).all() and (tok[L] == -7).all()
+    assert (out[:, 1:L + 1, :shift] == 7).all() and (out[:, 1:L + 1, shift + V:] == 7).all()
+
+
+def test_rows_between_rows():
+    # probabilities in the gaps that the logits' strides leave
+    B, V = 5, 640
+    buf = torch.zeros(B, 2, V, device=DEV)
+    z = logits(B, V, 6)
+    buf[:, 0] = z.to(DEV)
+    probs = S.filter_probs(buf[:, 0], 0.9, 20, probs=buf[:, 1])
+    assert torch.equal(buf[:, 0], z.to(DEV))
+    check(z, None, 0.9, 20, 1.0, 0.0, probs)
+    with pytest.raises(S.SpecVerifyError):
+        S.filter_probs(buf[:, 0], 0.9, 20, probs=buf[:, 0])
+    with pytest.raises(S.SpecVerifyError):
+        S.filter_probs(buf[:, 0], 0.9, 20, probs=buf.view(B, 2 * V)[:, 1:V + 1])
+
+
+def test_parameters_out_of_range_on_the_device():
+    V = 900
+    z = logits(8, V, 9)
+    u = torch.rand(8, generator=torch.Generator().manual_seed(4))
+    T = torch.tensor([1.0, -1.0, float("nan"), float("inf"), 1.0, 1.0, 1.0, 1.0])
+    k = torch.tensor([0, 0, 0, 0, -1, 0, 0, 2 ** 31 - 1], dtype=I32)
+    p = torch.tensor([1.0, 1.0, 1.0, 1.0, 1.0, 0.0, 1.0, 1.0])
+    mp = torch.tensor([0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 1.5, 0.0])
+    probs, tok = both(z, u, T, k, p, mp)
+    check(z, u, T, k, p, mp, probs, tok)
+    assert tok.tolist()[1:7] == [-1] * 6 and int(tok[0]) >= 0 and int(tok[7]) >= 0
+
+
+def test_temperatures_from_tiny_to_huge():
+    z = logits(4, 2000, 10)
+    u = torch.rand(4, generator=torch.Generator().manual_seed(5))
+    for T in (1e-45, 1e-30, 1e-5, 1e4, 1e30, 3e38):
+        for f in ((T, 0, 1.0, 0.0), (T, 10, 0.9, 0.0), (T, 0, 0.5, 0.0), (T, 0, 1.0, 0.5)):
+            probs, tok = both(z, u, *f)
+            check(z, u, *f, probs, tok)
+
+
+def test_streams_graphs_and_repeats():
+    V = 40000
+    T, k = torch.tensor([1.0, 0.8, 0.0]).to(DEV), torch.tensor([0, 30, 0], dtype=I32).to(DEV)
+    p = torch.tensor([0.9, 1.0, 1.0]).to(DEV)
+    a, b = (logits(3, V, i, BF).to(DEV) for i in (20, 21))
+    u = torch.rand(3, device=DEV)
+    ra, rb = (S.filter_probs(z, T, k, p, u=u) for z in (a, b))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        x, y = S.filter_probs(a, T, k, p, u=u, stream=s1), S.filter_probs(b, T, k, p, u=u, stream=s2)
+        t = S.sample_filtered(a, u, T, k, p, stream=s1)
+        torch.cuda.synchronize()
+        assert all(map(torch.equal, x + y, ra + rb)) and torch.equal(t, ra[1])
+    # two graphs, one workspace, replayed in turn between eager calls
+    ws = torch.empty(draft.filter_workspace_bytes(3, 1, V, BF), dtype=torch.uint8, device=DEV)
+    graphs = []
+    for z in (a, b):
+        st = z.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = S.filter_probs(st, T, k, p, u=u, workspace=ws)
+        graphs.append((g, st, res))
+    for i in range(4):
+        for (g, st, res), mine, other, want in zip(graphs, (a, b), (b, a), ((ra, rb), (rb, ra))):
+            st.copy_(mine if i % 2 == 0 else other)
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(map(torch.equal, res, want[i % 2]))
+            assert torch.equal(S.sample_filtered(a, u, T, k, p), ra[1])
+
+
+def test_many_rows_with_shared_parameters():
+    B, L, V = 130, 5, 700
+    g = torch.Generator().manual_seed(6)
+    z = logits(B * L, V, 30, BF).reshape(B, L, V)
+    T = torch.rand(B, generator=g) + 0.3
+    T[::9] = 0
+    k = torch.randint(0, 40, (B,), generator=g, dtype=I32)
+    p = 1 - torch.rand(B, generator=g) * 0.5
+    mp = torch.rand(B, generator=g) * 0.1
+    u = torch.rand(B, L, generator=g)
+    probs, tok = both(z, u, T, k, p, mp, BF)
+    assert check(z.reshape(-1, V), u.reshape(-1), T, k, p, mp, probs.reshape(-1, V), tok.reshape(-1), L) <= 2
+
+
+def test_draws_follow_the_distribution():
+    # chi-square of 20000 draws over a small kept set, 5 sigma
+    z = logits(1, 300, 31).expand(20000, 300).to(DEV)    # rows of stride 0
+    u = torch.rand(20000, generator=torch.Generator(device=DEV).manual_seed(7), device=DEV)
+    tok = S.sample_filtered(z, u, 0.9, 12, 0.97).cpu().numpy()
+    P, _ = OD.filtered(z[0].double().cpu().numpy(), 0.9, 12, 0.97)
+    n = np.bincount(tok, minlength=300)
+    kept = P > 0
+    assert n[~kept].sum() == 0
+    df = kept.sum() - 1
+    chi = ((n[kept] - 20000 * P[kept]) ** 2 / (20000 * P[kept])).sum()
+    assert chi < df + 5 * np.sqrt(2 * df)
+
+
+def test_python_refusals():
+    z = torch.zeros(3, 100, device=DEV)
+    u = torch.zeros(3, device=DEV)
+    with pytest.raises(TypeError):
+        S.sample_filtered(z.half(), u)
+    with pytest.raises(ValueError):
+        S.sample_filtered(z[0], u)
+    with pytest.raises(ValueError):
+        S.sample_filtered(z.t(), u)
+    with pytest.raises(ValueError):
+        S.sample_filtered(z, u[:2])
+    with pytest.raises(TypeError):
+        S.sample_filtered(z, u.double())
+    with pytest.raises(TypeError):
+        S.sample_filtered(z, u, 1.0, torch.zeros(3, device=DEV))
+    with pytest.raises(ValueError):
+        S.sample_filtered(z, u, torch.ones(2, device=DEV))
+    with pytest.raises(ValueError):
+        S.sample_filtered(z, u, torch.ones(3))
+    with pytest.raises(ValueError):
+        S.filter_probs(z, out_tokens=torch.zeros(3, dtype=I32, device=DEV))
+    with pytest.raises(TypeError):
+        S.filter_probs(z, probs=torch.zeros(3, 100, device=DEV), dtype=BF)
+    with pytest.raises(TypeError):
+        S.sample_filtered(z, u, "1")
+    for kw in (dict(temperature=-1.0), dict(top_k=-1), dict(top_p=0.0), dict(top_p=1.1), dict(min_p=2.0)):
+        with pytest.raises(S.SpecVerifyError):
+            S.sample_filtered(z, u, **kw)
+    with pytest.raises(S.SpecVerifyError) as e:
+        S.sample_filtered(z, u, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    assert e.value.status == binding.SPECV_EWORKSPACE
+    with pytest.raises(S.SpecVerifyError):
+        S.sample_filtered(z[:0], u[:0])
