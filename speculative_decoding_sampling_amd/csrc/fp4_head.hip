@@ -20,12 +20,13 @@
 #include "fp4.h"
 #include "fp8.h"
 #include "grid.h"
+#include "head_tile.h"
 #include "specverify_draft.h"
 
 namespace specv {
 
 typedef int fp4_i32x8 __attribute__((ext_vector_type(8)));
-typedef float fp4_f32x16 __attribute__((ext_vector_type(16)));
+using fp4_f32x16 = HeadF32x16;
 typedef __bf16 fp4_bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 fp4_bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -141,10 +142,6 @@ hipError_t launch_fp4_pack(const uint8_t* q, const uint8_t* scale, void* packed,
 template <bool H8, typename O>
 constexpr bool kFp4Exact = H8 && sizeof(O) == 4;
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p) {
-  return *reinterpret_cast<const uint4*>(p);
-}
-
 // A lane's part of a step of its hidden row: h is l / 32.
 template <bool H8, bool EXACT>
 struct Fp4Hidden {
@@ -196,13 +193,10 @@ __device__ __forceinline__ fp4_f32x16 fp4_step(const uint4& a, const uint4& lo, 
   }
 }
 
-__device__ __forceinline__ void f4_put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void f4_put(bf16_t* p, float v) { *p = bf16_bits(v); }
-
 // A workgroup owns 32 vocabulary rows and up to 32 hidden rows; its four waves
 // split the runs of 128 columns (every fourth one each) and add their sums
 // through LDS in a fixed order.
-template <bool H8, typename O>
+template <bool ONCE, bool H8, typename O>
 __global__ __launch_bounds__(kF4Threads) void fp4_skinny_kernel(
     const uint8_t* __restrict__ H, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ P,
     const uint8_t* __restrict__ ws, int M, int D, int V, int ngroup, O* __restrict__ out) {
@@ -225,8 +219,8 @@ __global__ __launch_bounds__(kF4Threads) void fp4_skinny_kernel(
 
   for (int r = wave; r < runs; r += kF4Waves) {
     const int s = 2 * r;
-    const uint4 a0 = load16(wrow + (size_t)s * kF4StepBytes);
-    const uint4 a1 = load16(wrow + (size_t)(s + 1) * kF4StepBytes);
+    const uint4 a0 = load16_weight<ONCE>(wrow + (size_t)s * kF4StepBytes);
+    const uint4 a1 = load16_weight<ONCE>(wrow + (size_t)(s + 1) * kF4StepBytes);
     const uint32_t sa = *reinterpret_cast<const uint16_t*>(wsc + (s / 4) * (kWave * 4) + s % 4);
     Fp4Hidden<H8, EXACT> b0, b1;
     b0.load(hrow, s, h);
@@ -244,8 +238,278 @@ __global__ __launch_bounds__(kF4Threads) void fp4_skinny_kernel(
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kF4Waves; ++w) s += red[w][m][v];
-    if (group * kF4Group + v < V) f4_put(out + (size_t)(m0 + m) * V + group * kF4Group + v, s);
+    if (group * kF4Group + v < V) head_put(out + (size_t)(m0 + m) * V + group * kF4Group + v, s);
   }
+}
+
+// Many hidden rows.  A workgroup of four waves owns 256 vocabulary rows (64 a
+// wave) and 32 MT hidden rows; two workgroups share a CU.  Each wave reads its
+// weights straight into registers, runs ahead; the hidden rows of a run, 128
+// bytes of each, are staged in LDS a run ahead, and every wave reads all of
+// them, each fragment feeding two products.  A run is two steps of 8-bit or
+// four of 4-bit states.
+//
+// Rows of a staged run have their eight 16-byte pieces swapped by row pair (row
+// r's piece p at slot p ^ ((r >> 1) & 7)), so that 16 consecutive rows cover
+// every bank once.
+//
+// Workgroups are numbered so that one XCD (every eighth block) takes
+// consecutive (vocabulary tile, row block) pairs, row blocks first: the
+// blocks that share weights run side by side under one L2.
+constexpr int kF4RowBytes = 128;                   // staged bytes of a hidden row
+constexpr int kF4TileGroups = kTileVocab / kF4Group;
+static_assert(kF4TileGroups == 2 * kF4Waves && kF4Threads == kHeadThreads, "two groups to a wave");
+
+template <int MT, bool H8, typename O>
+struct Fp4Tile {
+  static constexpr int kRows = MT * 32;
+  static constexpr int kBuf = kRows * kF4RowBytes;
+  static constexpr int kBytes = 2 * kBuf > HeadStore<O>::kBytes ? 2 * kBuf : HeadStore<O>::kBytes;
+  static constexpr int kSteps = H8 ? 2 : 4;        // of a run
+  static constexpr int kRing = MT <= 1 || H8 ? 4 : 2;   // runs of weights in registers
+};
+
+// The tile of 256 vocabulary ids and hidden rows m0 .. m0 + 32 MT - 1.
+template <int MT, bool ONCE, bool H8, typename O>
+__device__ __forceinline__ void fp4_tile(uint8_t* lds, uint32_t (&lsc)[2][2 * kF4Threads],
+                                         const uint8_t* __restrict__ H,
+                                         const uint8_t* __restrict__ hs,
+                                         const uint8_t* __restrict__ P,
+                                         const uint32_t* __restrict__ ws, int M, int D, int V,
+                                         int ngroup, int tile, int m0, O* __restrict__ out) {
+  using T = Fp4Tile<MT, H8, O>;
+  constexpr bool EXACT = kFp4Exact<H8, O>;
+  constexpr int kBuf = T::kBuf, RING = T::kRing, STEPS = T::kSteps;
+  static_assert(T::kRows <= kF4Threads, "one row's scales to a thread");
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int h = lane / 32, l32 = lane % 32;
+  const int steps = D / kF4Step, nj = (steps + 3) / 4;
+  const int nrun = (steps + STEPS - 1) / STEPS;
+  const int row_bytes = H8 ? D : D / 2;
+
+  // this wave's two packed groups; groups past V repeat the last (dropped)
+  const int g0 = min(tile * kF4TileGroups + wave * 2, ngroup - 1), g1 = min(g0 + 1, ngroup - 1);
+  const uint8_t* w0 = P + (size_t)g0 * steps * kF4StepBytes;
+  const uint8_t* w1 = P + (size_t)g1 * steps * kF4StepBytes;
+  const uint32_t* s0 = ws + (size_t)g0 * nj * kWave + lane;
+  const uint32_t* s1 = ws + (size_t)g1 * nj * kWave + lane;
+  const uint32_t lane16 = lane * 16;
+
+  // staging: this thread's pieces are tid + 256 j, eight to a row; rows past
+  // M repeat the last (dropped).  The last run of 4-bit states may be half one:
+  // their pieces past the row's end are zeros, whatever weights they meet.
+  const uint8_t* hb = H + (size_t)m0 * row_bytes;
+  const int left = M - 1 - m0;
+  uint32_t hoff[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) hoff[j] = (uint32_t)min(tid / 8 + 32 * j, left) * row_bytes;
+  const uint32_t piece = (tid % 8) * 16;
+  const int slot = (tid / 8) * kF4RowBytes + (((tid % 8) ^ ((tid / 16) & 7)) * 16);
+  const int nblock = H8 ? D / kFp8Block : D / kFp4Block;
+  const uint8_t* hsrow = hs + (size_t)(m0 + min(tid, left)) * nblock;
+
+  fp4_f32x16 acc[2][MT];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][t][r] = 0.f;
+
+  constexpr int kW = 2 * STEPS;                    // weight loads of a run
+  uint4 wr[RING][2][STEPS], st[MT];
+  // load i of the MT + kW of a run: staged hidden rows of run kb, then weights
+  // of run kbw (past the end: the last step again)
+  auto load = [&](int i, int kb, int kbw, uint4 (&d)[2][STEPS]) {
+    if (i < MT) {
+      const uint32_t at = (uint32_t)kb * kF4RowBytes + piece;
+      st[i] = load16(hb + hoff[i] + min(at, (uint32_t)row_bytes - 16));
+    } else {
+      const int a = (i - MT) / STEPS, s = (i - MT) % STEPS;
+      d[a][s] = load16_weight<ONCE>((a ? w1 : w0) + (size_t)min(kbw * STEPS + s, steps - 1) * kF4StepBytes +
+                                    lane16);
+    }
+  };
+  auto store_h = [&](int b, int kb) {
+    // (a mask: a branch would cut the product loop into blocks)
+    const uint32_t in = (uint32_t)kb * kF4RowBytes + piece < (uint32_t)row_bytes ? ~0u : 0u;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      uint4 v = st[j];
+      if constexpr (!H8) v = make_uint4(v.x & in, v.y & in, v.z & in, v.w & in);
+      *reinterpret_cast<uint4*>(lds + b * kBuf + slot + j * 32 * kF4RowBytes) = v;
+    }
+  };
+  // The rows' scales: 8 bits, bytes 4 g .. 4 g + 3 of a row as a word, one a
+  // run; 4 bits, the bytes of run g, those of each half of a wave as a word.
+  struct Scales {
+    uint32_t b[H8 ? 4 : 2];
+  };
+  auto scale_load = [&](int g) {
+    Scales x;
+    if constexpr (H8) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x.b[e] = hsrow[min(4 * g + e, nblock - 1)];
+    } else {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(hsrow);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) x.b[e] = p[min(2 * g + e, nblock / 4 - 1)];
+    }
+    return x;
+  };
+  auto scale_store = [&](int buf, const Scales& x) {
+    if constexpr (H8) {
+      lsc[buf][tid] = x.b[0] | x.b[1] << 8 | x.b[2] << 16 | x.b[3] << 24;
+    } else {
+      lsc[buf][tid] = __builtin_amdgcn_perm(x.b[1], x.b[0], 0x06040200u);
+      lsc[buf][tid + kF4Threads] = __builtin_amdgcn_perm(x.b[1], x.b[0], 0x07050301u);
+    }
+  };
+
+#pragma unroll
+  for (int i = 0; i < MT; ++i) load(i, 0, 0, wr[0]);
+  scale_store(0, scale_load(0));
+#pragma unroll
+  for (int r = 0; r < RING - 1; ++r)
+#pragma unroll
+    for (int i = MT; i < MT + kW; ++i) load(i, 0, r, wr[r]);
+  store_h(0, 0);
+  lds_barrier();
+
+  uint32_t sa0 = 0, sa1 = 0, sb[MT];
+  // run kb, the I-th of its group
+  auto run = [&](auto idx, int kb) {
+    constexpr int I = decltype(idx)::value;
+    const uint8_t* buf = lds + (I % 2) * kBuf + l32 * kF4RowBytes;
+    const uint4(&w)[2][STEPS] = wr[I % RING];
+    const int sw = (l32 >> 1) & 7;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {              // a step's products are kept together
+#pragma unroll
+      for (int l = s * (MT + kW) / STEPS; l < (s + 1) * (MT + kW) / STEPS; ++l)
+        load(l, kb + 1, kb + RING - 1, wr[(I + RING - 1) % RING]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint8_t* row = buf + t * 32 * kF4RowBytes;
+        uint4 lo, hi = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (!H8) {
+          lo = load16(row + (((2 * s + h) ^ sw) * 16));
+        } else {
+          lo = load16(row + (((4 * s + (EXACT ? 2 : 1) * h) ^ sw) * 16));
+          hi = load16(row + (((4 * s + (EXACT ? 2 * h + 1 : 2 + h)) ^ sw) * 16));
+        }
+        constexpr int IA = H8 ? 2 * (I % 2) : 0, IB = H8 ? I : 0;
+        if constexpr (H8) {
+          if (s == 0) {
+            acc[0][t] = fp4_step<H8, EXACT, IA, IB>(w[0][s], lo, hi, acc[0][t], sa0, sb[t]);
+            acc[1][t] = fp4_step<H8, EXACT, IA, IB>(w[1][s], lo, hi, acc[1][t], sa1, sb[t]);
+          } else {
+            acc[0][t] = fp4_step<H8, EXACT, IA + 1, IB>(w[0][s], lo, hi, acc[0][t], sa0, sb[t]);
+            acc[1][t] = fp4_step<H8, EXACT, IA + 1, IB>(w[1][s], lo, hi, acc[1][t], sa1, sb[t]);
+          }
+        } else {
+          auto both = [&](auto S) {
+            constexpr int B = decltype(S)::value;
+            acc[0][t] = fp4_step<H8, EXACT, B, B>(w[0][s], lo, hi, acc[0][t], sa0, sb[t]);
+            acc[1][t] = fp4_step<H8, EXACT, B, B>(w[1][s], lo, hi, acc[1][t], sa1, sb[t]);
+          };
+          if (s == 0) both(std::integral_constant<int, 0>{});
+          else if (s == 1) both(std::integral_constant<int, 1>{});
+          else if (s == 2) both(std::integral_constant<int, 2>{});
+          else both(std::integral_constant<int, 3>{});
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    store_h((I + 1) % 2, kb + 1);
+  };
+  using std::integral_constant;
+  if constexpr (H8) {
+    // groups of four runs: one word of the hidden rows' scales, two of the weights'
+    uint32_t n0[2] = {s0[0], s0[min(1, nj - 1) * kWave]}, n1[2] = {s1[0], s1[min(1, nj - 1) * kWave]};
+    for (int g = 0;; ++g) {
+      const Scales next = scale_load(g + 1);       // past the end: the last bytes (not used)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) sb[t] = lsc[g & 1][t * 32 + l32];
+      sa0 = n0[0];
+      sa1 = n1[0];
+      run(integral_constant<int, 0>{}, 4 * g);
+      lds_barrier();
+      if (4 * g + 1 == nrun) break;
+      run(integral_constant<int, 1>{}, 4 * g + 1);
+      lds_barrier();
+      if (4 * g + 2 == nrun) break;
+      sa0 = n0[1];
+      sa1 = n1[1];
+      n0[0] = s0[min(2 * g + 2, nj - 1) * kWave];
+      n1[0] = s1[min(2 * g + 2, nj - 1) * kWave];
+      run(integral_constant<int, 2>{}, 4 * g + 2);
+      lds_barrier();
+      if (4 * g + 3 == nrun) break;
+      n0[1] = s0[min(2 * g + 3, nj - 1) * kWave];
+      n1[1] = s1[min(2 * g + 3, nj - 1) * kWave];
+      run(integral_constant<int, 3>{}, 4 * g + 3);
+      scale_store((g + 1) & 1, next);
+      lds_barrier();
+      if (4 * g + 4 == nrun) break;
+    }
+  } else {
+    // every run has its own words
+    uint32_t n0 = s0[0], n1 = s1[0];
+    auto turn = [&](auto idx, int kb) {
+      constexpr int I = decltype(idx)::value;
+      const int next = min(kb + 1, nrun - 1);
+      const Scales nh = scale_load(next);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) sb[t] = lsc[I % 2][h * kF4Threads + t * 32 + l32];
+      sa0 = n0;
+      sa1 = n1;
+      n0 = s0[next * kWave];
+      n1 = s1[next * kWave];
+      run(idx, kb);
+      scale_store((I + 1) % 2, nh);
+      lds_barrier();
+    };
+    for (int kb = 0;; kb += RING) {
+      turn(integral_constant<int, 0>{}, kb);
+      if (kb + 1 == nrun) break;
+      turn(integral_constant<int, 1>{}, kb + 1);
+      if (kb + 2 == nrun) break;
+      if constexpr (RING == 4) {
+        turn(integral_constant<int, 2>{}, kb + 2);
+        if (kb + 3 == nrun) break;
+        turn(integral_constant<int, 3>{}, kb + 3);
+        if (kb + 4 == nrun) break;
+      }
+    }
+  }
+  head_store<MT>(lds, acc, tile, m0, M, V, out);
+}
+
+// The row blocks share the 32-row steps evenly, at most MT each.
+template <int MT, bool ONCE, bool H8, typename O>
+__global__ __launch_bounds__(kF4Threads, 2) void fp4_tile_kernel(
+    const uint8_t* __restrict__ H, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ P,
+    const uint32_t* __restrict__ ws, int M, int D, int V, int ngroup, int nrb, int nwork,
+    O* __restrict__ out) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Fp4Tile<MT, H8, O>::kBytes];
+  __shared__ uint32_t lsc[2][2 * kF4Threads];                // words past the rows are not read
+  const int per = (nwork + kXcds - 1) / kXcds;
+  const int work = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
+  if (work >= nwork) return;                                 // blockIdx.x / kXcds < per
+  const int tile = work / nrb, rb = work % nrb, all = (M + 31) / 32;
+  const int m0 = 32 * (rb * (all / nrb) + min(rb, all % nrb));
+  const int steps = all / nrb + (rb < all % nrb ? 1 : 0);
+  if (MT > 3 && steps == 3)
+    fp4_tile<MT < 3 ? MT : 3, ONCE, H8>(lds, lsc, H, hs, P, ws, M, D, V, ngroup, tile, m0, out);
+  else if (MT > 2 && steps == 2)
+    fp4_tile<MT < 2 ? MT : 2, ONCE, H8>(lds, lsc, H, hs, P, ws, M, D, V, ngroup, tile, m0, out);
+  else if (MT > 1 && steps == 1)
+    fp4_tile<1, ONCE, H8>(lds, lsc, H, hs, P, ws, M, D, V, ngroup, tile, m0, out);
+  else
+    fp4_tile<MT, ONCE, H8>(lds, lsc, H, hs, P, ws, M, D, V, ngroup, tile, m0, out);
 }
 
 struct Fp4Args {
@@ -254,13 +518,51 @@ struct Fp4Args {
   hipStream_t stream;
 };
 
-template <bool H8, typename O>
-hipError_t fp4_head(const Fp4Args& a, O* out) {
+template <int MT, bool ONCE, bool H8, typename O>
+hipError_t fp4_tiles(const Fp4Args& a, O* out) {
+  const int nrb = (a.M + 32 * MT - 1) / (32 * MT);
+  const size_t nwork = (size_t)((a.V + kTileVocab - 1) / kTileVocab) * nrb;
+  const size_t blocks = (nwork + kXcds - 1) / kXcds * kXcds;
+  fp4_tile_kernel<MT, ONCE, H8, O><<<dim3((unsigned)blocks), dim3(kF4Threads), 0, a.stream>>>(
+      a.H, a.hs, a.P, reinterpret_cast<const uint32_t*>(a.ws), a.M, a.D, a.V, fp4_groups(a.V), nrb,
+      (int)nwork, out);
+  return hipGetLastError();
+}
+
+template <bool ONCE, bool H8, typename O>
+hipError_t fp4_skinny(const Fp4Args& a, O* out) {
   const int ng = fp4_groups(a.V);
   const size_t blocks = (size_t)ng * ((a.M + 31) / 32);
-  fp4_skinny_kernel<H8, O><<<dim3((unsigned)blocks), dim3(kF4Threads), 0, a.stream>>>(
+  fp4_skinny_kernel<ONCE, H8, O><<<dim3((unsigned)blocks), dim3(kF4Threads), 0, a.stream>>>(
       a.H, a.hs, a.P, a.ws, a.M, a.D, a.V, ng, out);
   return hipGetLastError();
+}
+
+constexpr double kFp4CacheBytes = 256.0 * (1 << 20);
+
+// Which product: 0 the skinny one, MT = 1..4 row blocks of at most 32 MT hidden
+// rows.  At 32 rows the skinny one takes 99 us of 128256 x 4096, a tile 52.
+int fp4_choice(int M, int D, int V, bool h8, bool exact) {
+  if (M <= 16) return 0;
+  const int mt = (M + 31) / 32;
+  return exact ? (mt < 3 ? mt : 3) : mt < 4 ? mt : 4;
+}
+
+template <bool ONCE, bool H8, typename O>
+hipError_t fp4_run(const Fp4Args& a, int choice, O* out) {
+  if (choice == 0) return fp4_skinny<ONCE, H8>(a, out);
+  if (choice == 1) return fp4_tiles<1, ONCE, H8>(a, out);
+  if (choice == 2) return fp4_tiles<2, ONCE, H8>(a, out);
+  if constexpr (!kFp4Exact<H8, O>)                           // bfloat16 operands: 4 would spill
+    if (choice == 4) return fp4_tiles<4, ONCE, H8>(a, out);
+  return fp4_tiles<3, ONCE, H8>(a, out);
+}
+template <bool H8, typename O>
+hipError_t fp4_head(const Fp4Args& a, O* out) {
+  const int choice = fp4_choice(a.M, a.D, a.V, H8, kFp4Exact<H8, O>);
+  const int rows = choice == 0 ? 32 : 32 * choice;
+  return a.M <= rows && (double)a.V * a.D / 2 > kFp4CacheBytes ? fp4_run<true, H8>(a, choice, out)
+                                                                  : fp4_run<false, H8>(a, choice, out);
 }
 
 hipError_t launch_fp4_head(const uint8_t* hidden, bool h8, const uint8_t* hscale, const void* packed,

@@ -20,12 +20,13 @@
 // matrix core's own 32-wide blocks are.
 #include "fp8.h"
 #include "grid.h"
+#include "head_tile.h"
 #include "specverify_ops.h"
 
 namespace specv {
 
 typedef int fp8_i32x8 __attribute__((ext_vector_type(8)));
-typedef float fp8_f32x16 __attribute__((ext_vector_type(16)));
+using fp8_f32x16 = HeadF32x16;
 typedef __bf16 fp8_bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 fp8_bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -194,35 +195,6 @@ __device__ __forceinline__ fp8_f32x16 fp8_step(const Fp8Bytes& a, const Fp8Bytes
 template <typename O>
 constexpr bool kFp8Exact = sizeof(O) == 4;
 
-__device__ __forceinline__ void f8_put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void f8_put(bf16_t* p, float v) { *p = bf16_bits(v); }
-// Four consecutive logits, registers r .. r + 3 of an accumulator.
-__device__ __forceinline__ void f8_put4(float* p, const fp8_f32x16& c, int r) {
-  *reinterpret_cast<float4*>(p) = make_float4(c[r], c[r + 1], c[r + 2], c[r + 3]);
-}
-__device__ __forceinline__ void f8_put4(bf16_t* p, const fp8_f32x16& c, int r) {
-  uint2 w;
-  w.x = bf16_pair(c[r], c[r + 1]);
-  w.y = bf16_pair(c[r + 2], c[r + 3]);
-  *reinterpret_cast<uint2*>(p) = w;
-}
-
-__device__ __forceinline__ uint4 load16(const uint8_t* p) {
-  return *reinterpret_cast<const uint4*>(p);
-}
-
-// 16 bytes of a weight, past the caches where the call reads it only once.
-template <bool ONCE>
-__device__ __forceinline__ uint4 load16_weight(const uint8_t* p) {
-  if constexpr (!ONCE) {
-    return load16(p);
-  } else {
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-    return make_uint4(v.x, v.y, v.z, v.w);
-  }
-}
-
 // Bytes 4 g .. 4 g + 3 of a row of nkb scale bytes as a word, 127 past the
 // end.  No branches: a product loop that holds one is cut into blocks, and the
 // compiler then moves products across them and spills their accumulators.
@@ -293,16 +265,8 @@ __global__ __launch_bounds__(kF8Threads) void fp8_skinny_kernel(
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kF8Waves; ++w) s += red[w][m][v];
-    if (group * kF8Group + v < V) f8_put(out + (size_t)(m0 + m) * V + group * kF8Group + v, s);
+    if (group * kF8Group + v < V) head_put(out + (size_t)(m0 + m) * V + group * kF8Group + v, s);
   }
-}
-
-// LDS writes of this workgroup made visible at a barrier, global loads left
-// in flight.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Many hidden rows.  A workgroup of four waves owns 256 vocabulary rows (64 a
@@ -324,21 +288,16 @@ __device__ __forceinline__ void lds_barrier() {
 // Workgroups are numbered so that one XCD (every eighth block) takes
 // consecutive (vocabulary tile, row block) pairs, row blocks first: the
 // blocks that share weights run side by side under one L2.
-constexpr int kTileVocab = 256;
 constexpr int kTileGroups = kTileVocab / kF8Group;
-constexpr int kXcds = 8;
 static_assert(kTileGroups == 2 * kF8Waves, "two packed groups to a wave");
 
 // A tile's LDS: two runs of staged hidden rows, in whose place the epilogue
-// moves 32 rows of bfloat16 logits or 16 of float32 at a time; two words of the
-// rows' scales.
+// moves the logits; two words of the rows' scales.
 template <int MT, typename O>
 struct Fp8Tile {
   static constexpr int kRows = MT * 32;
   static constexpr int kBuf = kRows * kFp8Block;
-  static constexpr int kTrStride = kTileVocab + 16 / (int)sizeof(O);
-  static constexpr int kTrRows = 64 / (int)sizeof(O);
-  static constexpr int kTrBytes = kTrRows * kTrStride * (int)sizeof(O);
+  static constexpr int kTrBytes = HeadStore<O>::kBytes;
   static constexpr int kBytes = 2 * kBuf > kTrBytes ? 2 * kBuf : kTrBytes;
   static constexpr int kRing = MT <= 2 ? 4 : 2;              // runs of weights in registers
 };
@@ -352,7 +311,7 @@ __device__ __forceinline__ void fp8_tile(uint8_t* lds, uint32_t (&lsc)[2][kF8Thr
                                          const uint32_t* __restrict__ ws, int M, int D, int V,
                                          int ngroup, int tile, int m0, O* __restrict__ out) {
   using T = Fp8Tile<MT, O>;
-  constexpr int kBuf = T::kBuf, kTrStride = T::kTrStride, kTrRows = T::kTrRows, RING = T::kRing;
+  constexpr int kBuf = T::kBuf, RING = T::kRing;
   static_assert(T::kRows <= kF8Threads, "one row's scales to a thread");
   static_assert(4 % RING == 0, "the weight ring indexes statically over a group of runs");
   const int tid = threadIdx.x, lane = tid % kWave;
@@ -465,66 +424,7 @@ __device__ __forceinline__ void fp8_tile(uint8_t* lds, uint32_t (&lsc)[2][kF8Thr
     sa1 = n1;
   }
 
-  // acc[a][t][r] is the logit of row 32 t + l32 of the block and vocabulary id
-  // 64 wave + 32 a + 8 (r / 4) + r % 4 + 4 h of the tile.
-  // They leave through LDS, so that a wave's stores cover consecutive ids: 16
-  // bytes a lane where every row starts 16-byte aligned, else two bfloat16
-  // logits that share an aligned word, or one float32 logit (stored straight
-  // from the accumulators an odd V cost 31 instead of 17 us at 320 x 20001 x
-  // 1152).
-  const int vb = wave * 64 + 4 * h;
-  const int v0 = tile * kTileVocab, nv = min(kTileVocab, V - v0);
-  constexpr int kVec = 16 / sizeof(O);
-  const bool whole = V % kVec == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-  O* tr = reinterpret_cast<O*>(lds);
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int part = 0; part < 32 / kTrRows; ++part) {
-      const int r0 = t * 32 + part * kTrRows;               // first row of the part in the block
-      if (32 == kTrRows || l32 / kTrRows == part) {
-        O* row = tr + (l32 % kTrRows) * kTrStride + vb;
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) f8_put4(row + 32 * a + 8 * q, acc[a][t], 4 * q);
-      }
-      lds_barrier();
-      if (whole) {
-#pragma unroll
-        for (int i = 0; i < kTrRows * kTileVocab / kVec / kF8Threads; ++i) {
-          const int p = tid + i * kF8Threads, row = p / (kTileVocab / kVec);
-          const int c = p % (kTileVocab / kVec) * kVec;
-          if (m0 + r0 + row < M && c < nv)
-            *reinterpret_cast<uint4*>(out + (size_t)(m0 + r0 + row) * V + v0 + c) =
-                *reinterpret_cast<const uint4*>(tr + row * kTrStride + c);
-        }
-      } else {
-        constexpr int kLog = 4 / sizeof(O);                  // logits of a 4-byte store
-#pragma unroll
-        for (int i = 0; i < kTrRows * kTileVocab / kLog / kF8Threads; ++i) {
-          const int p = tid + i * kF8Threads, row = p / (kTileVocab / kLog);
-          if (m0 + r0 + row >= M) continue;
-          O* dst = out + (size_t)(m0 + r0 + row) * V + v0;
-          const O* src = tr + row * kTrStride;
-          if constexpr (sizeof(O) == 4) {
-            const int c = p % kTileVocab;
-            if (c < nv) dst[c] = src[c];
-          } else {
-            // aligned words start at the row's first logit or its second; a
-            // first or last logit without a partner is stored alone
-            const int odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
-            const int c = odd + 2 * (p % (kTileVocab / 2));
-            if (odd && c == 1) dst[0] = src[0];
-            if (c + 1 < nv)
-              *reinterpret_cast<uint32_t*>(dst + c) = (uint32_t)src[c] | (uint32_t)src[c + 1] << 16;
-            else if (c < nv)
-              dst[c] = src[c];
-          }
-        }
-      }
-      lds_barrier();
-    }
+  head_store<MT>(lds, acc, tile, m0, M, V, out);
 }
 
 // The row blocks share the 32-row steps evenly, at most MT each: as many rows
