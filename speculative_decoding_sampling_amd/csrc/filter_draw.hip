@@ -17,6 +17,21 @@
 // their order, so that the histograms may be built with atomics, and n tokens
 // are off by at most n 2^-(s+1) of the largest weight.  The sums of a draw are
 // float64 in a fixed order.
+//
+// Split.  A row is cut into groups, one 16-byte vector for each lane of a wave,
+// and segments of four groups.
+//  stats    streams all rows, one wave a segment: each group's largest logit and,
+//           where they will be needed, each segment's sum of weights.
+//  plan     one workgroup a row: its maximum and total; finishes greedy and
+//           unfiltered rows; for the others a bracket [lo, hi) of logits that
+//           holds the threshold: from the groups' maxima for top-k, from a sample of
+//           the row for top-p, the threshold itself for min-p.
+//  collect  one wave a segment, those that reach the bracket: the sum of weights
+//           from hi up, and the logits in the bracket.
+//  row      one workgroup a row: the threshold among the collected logits, checked
+//           against the sums (where the sample misled, the search runs over the
+//           row itself, from a bound that holds always), and the draw.
+//  probs    writes the probabilities, reading the groups that hold kept tokens.
 #include "common.h"
 #include "exp64.h"
 #include "fp8.h"
@@ -29,21 +44,30 @@ namespace specv {
 constexpr int kFdThreads = 1024;
 constexpr int kFdWaves = kFdThreads / kWave;
 constexpr int kFdBins = 2 * kFdThreads;             // of a round of the search
-constexpr int kFdGroups = 4;                        // vectors per lane of a segment
-constexpr int kFdSegVecs = kFdGroups * kWave;       // a segment: one wave's load of 4 KB
-// segments of the longest row, which may start inside a vector (float32 has more)
-constexpr int kFdMaxSegs = SPECV_MAX_V / (kFdSegVecs * 4) + 1;
+constexpr int kFdGroups = 4;                        // groups of a segment
+constexpr int kFdSegVecs = kFdGroups * kWave;       // 4 KB of logits
+constexpr int kFdStatThreads = 256;
+constexpr int kFdPlanThreads = 512;
+constexpr int kFdSlot = 256;                        // logits in the bracket that a segment can hold
+constexpr int kFdSampleBins = 2 * kFdPlanThreads;
 
 enum FdKind : int { kFdError = 0, kFdGreedy = 1, kFdDraw = 2 };
+// What is left to do for a row after its plan.
+enum FdNeed : int { kFdDone = 0, kFdSums = 1, kFdTopK = 2, kFdTopP = 4 };
 
-// What the row kernel leaves for the kernel that writes the probabilities.
+// A row's plan, and what the kernel that writes the probabilities reads.
 struct FdPlan {
   int kind;
+  int need;
   int best;          // greedy: the token
-  float m, tau;      // largest logit; a token is kept iff its logit >= tau
-  double invT, invS;
+  float m, tau;      // largest logit; a token is kept iff its logit >= tau (before the row
+                     // kernel: by min-p alone)
+  float lo, hi;      // the bracket
+  float bound;       // no token below it is kept by top-p
+  double invT, invS, Z;
+  double pad;
 };
-static_assert(sizeof(FdPlan) == 32, "FdPlan is 32 bytes");
+static_assert(sizeof(FdPlan) == 64, "FdPlan is 64 bytes");
 
 struct FdArgs {
   const void* z;
@@ -57,6 +81,12 @@ struct FdArgs {
   void* probs;
   long long psb, psl;
   FdPlan* plans;                    // [B L]
+  float4* gmax;                     // [B L][nseg] largest logit of each group, NaN for a bad one
+  double* ssum;                     // [B L][nseg] weights against the segment's largest logit, then
+                                    // (collect) against the row's, from hi up
+  uint32_t* slot_n;                 // [B L][nseg] logits in the bracket
+  float* slots;                     // [B L][nseg][kFdSlot] those logits, in order
+  int nseg, list_cap;
 };
 
 // A row as aligned 16-byte vectors.  The row may start inside the first one:
@@ -101,47 +131,10 @@ __device__ __forceinline__ FdParams fd_params(const specv_filters_t& f, int b) {
   return r;
 }
 
-struct FdShared {
-  double tbl[SPECV_EXP64_N];
-  unsigned long long mass[kFdBins];
-  uint32_t count[kFdBins];
-  double seg[kFdMaxSegs];
-  unsigned long long wave_u64[kFdWaves];
-  uint32_t wave_u32[kFdWaves];
-  float wave_f32[kFdWaves];
-  int found;
-  unsigned long long above;
-};
-
-__device__ __forceinline__ float fd_block_max(FdShared& s, float v) {
-  v = wave_max(v);
-  if (threadIdx.x % kWave == 0) s.wave_f32[threadIdx.x / kWave] = v;
-  __syncthreads();
-  float r = s.wave_f32[0];
-#pragma unroll
-  for (int w = 1; w < kFdWaves; ++w) r = fmaxf(r, s.wave_f32[w]);
-  __syncthreads();
-  return r;
-}
-__device__ __forceinline__ uint32_t fd_block_min(FdShared& s, uint32_t v) {
-  v = wave_reduce_u32(v, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
-  if (threadIdx.x % kWave == 0) s.wave_u32[threadIdx.x / kWave] = v;
-  __syncthreads();
-  uint32_t r = s.wave_u32[0];
-#pragma unroll
-  for (int w = 1; w < kFdWaves; ++w) r = min(r, s.wave_u32[w]);
-  __syncthreads();
-  return r;
-}
-__device__ __forceinline__ unsigned long long fd_block_sum(FdShared& s, unsigned long long v) {
-  v = wave_incl_scan_u64(v);
-  if (threadIdx.x % kWave == kWave - 1) s.wave_u64[threadIdx.x / kWave] = v;
-  __syncthreads();
-  unsigned long long r = 0;
-#pragma unroll
-  for (int w = 0; w < kFdWaves; ++w) r += s.wave_u64[w];
-  __syncthreads();
-  return r;
+// Whether a row's sums of weights are wanted: for the mass that top-p is a part
+// of, or for a draw from all tokens.
+__device__ __forceinline__ bool fd_wants_sums(const FdParams& f, int V) {
+  return f.ok && f.T > 0.f && (f.k == 0 || f.k >= V) && (f.p < 1.f || f.mp == 0.f);
 }
 
 // exp((z - m) / T), at most 1.
@@ -149,85 +142,259 @@ __device__ __forceinline__ double fd_weight(float z, double m, double invT, cons
   return exp64(((double)z - m) * invT, tbl);
 }
 
-// The block's pass over a row: f(vector, elements, first id).
-template <typename T, typename F>
-__device__ __forceinline__ void fd_scan(const FdRow<T>& row, F f) {
-  const int nv = row.vecs();
-  for (int q = threadIdx.x; q < nv; q += kFdThreads) {
-    float v[FdRow<T>::N];
-    row.load(q, v);
-    f(v, row.first(q));
+// A row's groups: one wave a segment.
+template <typename T>
+__global__ __launch_bounds__(kFdStatThreads) void filter_stats_kernel(FdArgs a, int nblk) {
+  constexpr int N = FdRow<T>::N;
+  __shared__ double tbl[SPECV_EXP64_N];
+  const int r = blockIdx.x / nblk, b = r / a.L, l = r % a.L;
+  const int lane = threadIdx.x % kWave;
+  const int g = (blockIdx.x % nblk) * (kFdStatThreads / kWave) + threadIdx.x / kWave;
+  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
+  const FdParams f = fd_params(a.f, b);
+  const bool sums = fd_wants_sums(f, a.V);
+  float v[kFdGroups][N];
+#pragma unroll
+  for (int j = 0; j < kFdGroups; ++j) row.load(g * kFdSegVecs + j * kWave + lane, v[j]);
+  if (sums) {
+    exp64_stage_table<kFdStatThreads>(tbl);
+    __syncthreads();
+  }
+  if (g >= a.nseg) return;
+  float top[kFdGroups], m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kFdGroups; ++j) {
+    bool bad = false;
+    top[j] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      top[j] = fmaxf(top[j], v[j][i]);
+      bad = bad || !(v[j][i] < INFINITY);            // NaN or +inf
+    }
+    top[j] = wave_max(top[j]);
+    m = fmaxf(m, top[j]);
+    if (__any(bad)) top[j] = __builtin_nanf("");
+  }
+  double w = 0.0;
+  if (sums && m > -INFINITY) {
+    const double invT = 1.0 / (double)f.T;
+#pragma unroll
+    for (int j = 0; j < kFdGroups; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) w += fd_weight(v[j][i], m, invT, tbl);
+    w = wave_sum(w);
+  }
+  if (lane == 0) {
+    a.gmax[(size_t)r * a.nseg + g] = make_float4(top[0], top[1], top[2], top[3]);
+    if (sums) a.ssum[(size_t)r * a.nseg + g] = w;
   }
 }
 
-// The search for a threshold, by the whole block: the key of the lowest kept
-// value, where a value is kept if what lies above it is below the target.
-// Each round sorts the keys of the bracket [lo, hi] into bins by count, and by
-// mass where that is what the target is about, finds the bin where the running
-// sum from the top reaches the target and goes on inside it, until it holds one
-// value (or one key: ties go together).
-template <bool MASS, typename T, typename W>
-__device__ uint32_t fd_search(FdShared& s, const FdRow<T>& row, uint32_t lo, uint32_t hi,
-                              double target, W weight) {
-  unsigned long long above = 0;
+// LDS of the plan and row kernels; behind it, sized by the call: seg[nseg]
+// (double), picks[nseg] (uint32) and, for the row kernel, list[cap] (float).
+struct FdShared {
+  double tbl[SPECV_EXP64_N];
+  unsigned long long mass[kFdBins];
+  uint32_t count[kFdBins];
+  unsigned long long wave_u64[kFdWaves];
+  uint32_t wave_u32[kFdWaves];
+  uint32_t npick;
+  unsigned long long above;
+};
+
+template <int WAVES>
+__device__ __forceinline__ uint32_t fd_block_max(FdShared& s, uint32_t v) {
+  v = wave_max_u32(v);
+  if (threadIdx.x % kWave == 0) s.wave_u32[threadIdx.x / kWave] = v;
+  __syncthreads();
+  uint32_t r = s.wave_u32[0];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) r = max(r, s.wave_u32[w]);
+  __syncthreads();
+  return r;
+}
+// The sum of all threads' values before this one's, and of all.
+template <int WAVES>
+__device__ __forceinline__ unsigned long long fd_block_scan(FdShared& s, unsigned long long v,
+                                                            unsigned long long& total) {
+  const unsigned long long incl = wave_incl_scan_u64(v);
+  const int wave = threadIdx.x / kWave;
+  if (threadIdx.x % kWave == kWave - 1) s.wave_u64[wave] = incl;
+  __syncthreads();
+  unsigned long long before = incl - v, sum = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const unsigned long long x = s.wave_u64[w];
+    if (w < wave) before += x;
+    sum += x;
+  }
+  __syncthreads();
+  total = sum;
+  return before;
+}
+template <int WAVES>
+__device__ __forceinline__ double fd_block_sum(FdShared& s, double v) {
+  v = wave_sum(v);
+  if (threadIdx.x % kWave == 0) s.wave_u64[threadIdx.x / kWave] = __double_as_longlong(v);
+  __syncthreads();
+  double r = 0.0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) r += __longlong_as_double(s.wave_u64[w]);
+  __syncthreads();
+  return r;
+}
+
+// Order-preserving key of a logit: 32 bits, or the 16 that a bfloat16 one has.
+// unkey of a 16-bit one is a threshold that parts it from the value below.
+template <typename T>
+__device__ __forceinline__ uint32_t fd_key(float f) {
+  return sizeof(T) == 2 ? fkey(f) >> 16 : fkey(f);
+}
+template <typename T>
+__device__ __forceinline__ float fd_unkey(uint32_t k) {
+  return unkey(sizeof(T) == 2 ? k << 16 : k);
+}
+template <typename T>
+constexpr uint32_t kFdLowest = sizeof(T) == 2 ? (kNegInfKey >> 16) + 1 : kNegInfKey + 1;
+
+// Which of a segment's groups reach tau, as four bits.
+__device__ __forceinline__ uint32_t fd_reach(const float4& t, float tau) {
+  return (t.x >= tau ? 1u : 0u) | (t.y >= tau ? 2u : 0u) | (t.z >= tau ? 4u : 0u) |
+         (t.w >= tau ? 8u : 0u);
+}
+
+// The segments that hold a group reaching tau, in any order: the segment's
+// number above the four bits.
+__device__ __forceinline__ uint32_t fd_pick(FdShared& s, uint32_t* picks, const float4* gmax,
+                                            int nseg, float tau) {
+  if (threadIdx.x == 0) s.npick = 0;
+  __syncthreads();
+  for (int g = threadIdx.x; g < nseg; g += kFdThreads) {
+    const uint32_t bits = fd_reach(gmax[g], tau);
+    if (bits) picks[atomicAdd(&s.npick, 1u)] = (uint32_t)g << 4 | bits;
+  }
+  __syncthreads();
+  return s.npick;
+}
+
+// The vectors of a picked segment, those of groups that were not picked as -inf.
+// Their loads repeat a picked group's, so that all are in flight at once.
+template <typename T>
+__device__ __forceinline__ void fd_load(const FdRow<T>& row, uint32_t pick, int lane,
+                                        float (&v)[kFdGroups][FdRow<T>::N]) {
+  const int q = (int)(pick >> 4) * kFdSegVecs + lane, any = __ffs((int)(pick & 15u)) - 1;
+#pragma unroll
+  for (int j = 0; j < kFdGroups; ++j) row.load(q + (pick >> j & 1u ? j : any) * kWave, v[j]);
+#pragma unroll
+  for (int j = 0; j < kFdGroups; ++j)
+    if (!(pick >> j & 1u)) {
+#pragma unroll
+      for (int i = 0; i < FdRow<T>::N; ++i) v[j][i] = -INFINITY;
+    }
+}
+
+// The logits that a search is about: the list, or the picked segments again.
+template <typename T>
+struct FdSource {
+  FdRow<T> row;
+  const uint32_t* picks;
+  uint32_t npick;
+  const float* list;
+  uint32_t n;
+  bool listed;
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    if (listed) {
+      for (uint32_t i = threadIdx.x; i < n; i += kFdThreads) f(list[i]);
+    } else {
+      for (uint32_t e = threadIdx.x / kWave; e < npick; e += kFdWaves) {
+        float v[kFdGroups][FdRow<T>::N];
+        fd_load(row, picks[e], threadIdx.x % kWave, v);
+#pragma unroll
+        for (int j = 0; j < kFdGroups; ++j)
+#pragma unroll
+          for (int i = 0; i < FdRow<T>::N; ++i) f(v[j][i]);
+      }
+    }
+  }
+};
+
+// What a search finds: the key of the lowest kept value, and whether the target
+// is reached there (if not all of the bracket is kept).
+struct FdFound {
+  uint32_t low;
+  bool reached;
+};
+
+// The search for a threshold, by a block of THREADS: a value is kept if what lies
+// above it (`above` before the bracket) is below the target.  Each round sorts
+// the keys of the bracket [lo, hi] into bins by count, and by mass where that is
+// what the target is about, finds the bin where the running sum from the top
+// reaches the target and goes on inside it, until it holds one value (or one key:
+// ties go together).  A BOUND takes one round.
+template <int THREADS, bool MASS, bool BOUND, typename Each, typename W>
+__device__ __forceinline__ FdFound fd_search(FdShared& s, uint32_t lo, uint32_t hi,
+                                             unsigned long long above, double target, Each each,
+                                             W weight) {
+  constexpr int kBins = 2 * THREADS, kBits = THREADS == 1024 ? 11 : 10, kWaves = THREADS / kWave;
+  static_assert(kBins == 1 << kBits && kBins <= kFdBins, "two bins to a thread");
   const int t = threadIdx.x, lane = t % kWave, wave = t / kWave;
-  for (;;) {
-    const int bits = 32 - __clz((int)((hi - lo) | 1u));
-    const int sh = max(bits - 11, 0);
-    static_assert(kFdBins == 1 << 11, "a round takes 11 bits of the key");
-    for (int i = t; i < kFdBins; i += kFdThreads) {
+  bool reached = false;
+  for (bool first_round = true;; first_round = false) {
+    const int sh = max(32 - __clz((int)((hi - lo) | 1u)) - kBits, 0);
+    for (int i = t; i < kBins; i += THREADS) {
       s.count[i] = 0;
       if (MASS) s.mass[i] = 0;
     }
-    if (t == 0) s.found = -1;
     __syncthreads();
-    fd_scan(row, [&](const float* v, int) {
-#pragma unroll
-      for (int i = 0; i < FdRow<T>::N; ++i) {
-        const uint32_t key = fkey(v[i]);
-        if (key >= lo && key <= hi) {
-          const int b = (int)((key - lo) >> sh);
-          atomicAdd(&s.count[b], 1u);
-          if (MASS) atomicAdd(&s.mass[b], weight(v[i]));
-        }
+    each([&](uint32_t key, float z) {
+      if (key >= lo && key <= hi) {
+        const int b = (int)((key - lo) >> sh);
+        atomicAdd(&s.count[b], 1u);
+        if (MASS) atomicAdd(&s.mass[b], weight(z));
       }
     });
     __syncthreads();
     // thread t owns bins top - 2 t and the one below: running sums from the top
-    const int b0 = kFdBins - 1 - 2 * t, b1 = b0 - 1;
-    const unsigned long long x0 = MASS ? s.mass[b0] : s.count[b0];
-    const unsigned long long x1 = MASS ? s.mass[b1] : s.count[b1];
+    const int b0 = kBins - 1 - 2 * t, b1 = b0 - 1;
+    const uint32_t c0 = s.count[b0], c1 = s.count[b1];
+    const unsigned long long x0 = MASS ? s.mass[b0] : c0;
+    const unsigned long long x1 = MASS ? s.mass[b1] : c1;
     const unsigned long long incl = wave_incl_scan_u64(x0 + x1);
     if (lane == kWave - 1) s.wave_u64[wave] = incl;
     __syncthreads();
     unsigned long long before = above + incl - (x0 + x1);
-    for (int w = 0; w < wave; ++w) before += s.wave_u64[w];
-    // the lowest bin that holds something and has less than the target above
-    int mine = -1;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) before += w < wave ? s.wave_u64[w] : 0ull;
+    // the lowest bin that holds something and has less than the target above:
+    // its number, in bit 31 whether it holds one value only, in bit 30 whether
+    // the target is reached with it
+    uint32_t mine = 0xffffffffu;
     unsigned long long mine_above = 0;
-    if (s.count[b0] && (double)before < target) {
-      mine = b0;
-      mine_above = before;
-    }
-    if (s.count[b1] && (double)(before + x0) < target) {
-      mine = b1;
-      mine_above = before + x0;
-    }
-    const uint64_t some = __ballot(mine >= 0);
-    if (some && lane == 63 - __clzll((long long)some)) s.wave_u32[wave] = (uint32_t)mine;
-    if (!some && lane == 0) s.wave_u32[wave] = 0xffffffffu;
+    auto take = [&](int bin, uint32_t c, unsigned long long x, unsigned long long over) {
+      if (c == 0 || !((double)over < target)) return;
+      mine = (uint32_t)bin | (c == 1u ? 1u << 31 : 0u) | ((double)(over + x) >= target ? 1u << 30 : 0u);
+      mine_above = over;
+    };
+    take(b0, c0, x0, before);
+    take(b1, c1, x1, before + x0);
+    const uint64_t some = __ballot(mine != 0xffffffffu);
+    const int src = some ? 63 - __clzll((long long)some) : 0;
+    if (lane == src) s.wave_u32[wave] = mine;
     __syncthreads();
-    int bin = -1;
-    for (int w = 0; w < kFdWaves; ++w)
-      if (s.wave_u32[w] != 0xffffffffu) bin = (int)s.wave_u32[w];
-    if (bin >= 0 && mine == bin) s.above = mine_above;
+    uint32_t found = 0xffffffffu;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const uint32_t x = s.wave_u32[w];
+      if (x != 0xffffffffu) found = x;
+    }
+    if (found != 0xffffffffu && mine == found) s.above = mine_above;
     __syncthreads();
-    if (bin < 0) return lo;                          // nothing in the bracket
-    const uint32_t base = lo + ((uint32_t)bin << sh);
-    const bool last = sh == 0 || s.count[bin] == 1u;
+    if (found == 0xffffffffu) return {lo, reached};  // nothing in the bracket
+    if (first_round) reached = found >> 30 & 1u;
+    const uint32_t base = lo + ((found & (kFdBins - 1)) << sh);
     above = s.above;
-    __syncthreads();
-    if (last) return base;
+    if (BOUND || sh == 0 || found >> 31) return {base, reached};
     lo = base;
     hi = base + ((1u << sh) - 1u);
   }
@@ -254,150 +421,455 @@ __device__ __forceinline__ float fd_min_p_threshold(float m, double invT, float 
   return unkey(hi);
 }
 
-// One workgroup a row.
+// The draw from a row's segment masses seg (in LDS), by one wave: S their sum,
+// and where a token is wanted the first whose running sum exceeds u S, or where
+// rounding leaves none the last with weight.
 template <typename T>
-__global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
-  __shared__ FdShared s;
-  const int r = blockIdx.x, b = r / a.L, l = r % a.L;
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+__device__ __forceinline__ int fd_draw(const FdRow<T>& row, const double* seg, int nseg, bool token,
+                                       float u, float tau, float m, double invT, const double* tbl,
+                                       double& S) {
   constexpr int N = FdRow<T>::N;
-  if (threadIdx.x < SPECV_EXP64_N) s.tbl[threadIdx.x] = kExp64Table[threadIdx.x];
-  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
-  const FdParams f = fd_params(a.f, b);
-  const float u = a.tokens ? a.u[(size_t)b * a.usb + (size_t)l * a.usl] : 0.f;
-
-  float m = -INFINITY;
-  bool bad = false;
-  fd_scan(row, [&](const float* v, int) {
+  const int lane = threadIdx.x % kWave;
+  // lane l sums segments l per .. l per + per - 1
+  const int per = (nseg + kWave - 1) / kWave;
+  const int g0 = min(lane * per, nseg), g1 = min(g0 + per, nseg);
+  double mine = 0.0;
+  for (int g = g0; g < g1; ++g) mine += seg[g];
+  const double incl = wave_incl_scan(mine);
+  S = lane_value(incl, kWave - 1);
+  if (!token) return -1;
+  const double target = (double)u * S;
+  double run = wave_shr1(incl), at = 0.0, last_at = 0.0;
+  int pick = -1, last = -1;
+  for (int g = g0; g < g1; ++g) {
+    const double w = seg[g];
+    if (w > 0.0) {
+      last = g;
+      last_at = run;
+      if (pick < 0 && run + w > target) {
+        pick = g;
+        at = run;
+      }
+    }
+    run += w;
+  }
+  const uint64_t over = __ballot(pick >= 0), some = __ballot(last >= 0);
+  const int src = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)some);
+  const int g = lane_value(over ? pick : last, src);
+  double base = lane_value(over ? at : last_at, src);
+  // inside it: the same over lanes, then over a lane's elements
+  float v[kFdGroups][N];
+  fd_load(row, (uint32_t)g << 4 | 15u, lane, v);
+  int y = -1, end = -1;
+#pragma unroll
+  for (int j = 0; j < kFdGroups; ++j) {
+    const int e = row.first(g * kFdSegVecs + j * kWave + lane);
+    double w[N], sum = 0.0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      m = fmaxf(m, v[i]);
-      bad = bad || !(v[i] < INFINITY);               // NaN or +inf
+      w[i] = v[j][i] >= tau && v[j][i] > -INFINITY ? fd_weight(v[j][i], m, invT, tbl) : 0.0;
+      sum += w[i];
     }
-  });
-  bad = __syncthreads_or(bad);
-  m = fd_block_max(s, m);
-  const bool ok = f.ok && !bad && m > -INFINITY && u >= 0.f && u < 1.f;
-  FdPlan plan = {kFdError, -1, m, m, 0.0, 0.0};
+    const double in = wave_incl_scan(sum);
+    double here = base + wave_shr1(in);
+    int first = -1, tail = -1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      here += w[i];
+      if (w[i] > 0.0) {
+        tail = e + i;
+        if (first < 0 && here > target) first = tail;
+      }
+    }
+    const uint64_t hit = __ballot(first >= 0), any = __ballot(tail >= 0);
+    if (hit && y < 0) y = lane_value(first, __ffsll((unsigned long long)hit) - 1);
+    if (any) end = lane_value(tail, 63 - __clzll((long long)any));
+    base += lane_value(in, kWave - 1);
+  }
+  return y < 0 ? end : y;
+}
+
+// The bracket of a top-p threshold from a sample of the row.  With M(x) the mass
+// of the tokens x or more below the maximum (in units of T), the threshold lies
+// where M falls below B = (1 - p) Z.  The sample gives M as scale sum w; tokens
+// that weigh at most w = exp(-x) leave it uncertain by some sqrt(scale w M), and by
+// a few of those tokens where there are few: lo is the highest x at which M and
+// four deviations and eight tokens are below B, hi the lowest at which M less
+// those is above it.  Nothing rests on it but the time: the row kernel checks.
+template <typename T>
+__device__ __forceinline__ void fd_sample(FdShared& s, const FdRow<T>& row, float m, double invT,
+                                          double T64, double B, double width, double unit, float& lo,
+                                          float& hi) {
+  constexpr int N = FdRow<T>::N, kChunk = 16, kWaves = kFdPlanThreads / kWave;
+  const int t = threadIdx.x, chunks = (row.vecs() + kChunk - 1) / kChunk;
+  constexpr int kChunks = 8192 / (kChunk * N);       // 8192 tokens, in pieces of 256 bytes
+  const int n = min(chunks, kChunks);
+  for (int i = t; i < kFdSampleBins; i += kFdPlanThreads) s.mass[i] = 0;
+  __syncthreads();
+  const double per = kFdSampleBins / width;
+  unsigned long long tail = 0;
+  constexpr int kSweeps = kChunks * kChunk / kFdPlanThreads;
+  float v[kSweeps][N];
+#pragma unroll
+  for (int i = 0; i < kSweeps; ++i) {
+    const int c = i * (kFdPlanThreads / kChunk) + t / kChunk;
+    const int q = (int)((long long)c * chunks / n) * kChunk + t % kChunk;
+    row.load(c < n ? q : row.vecs(), v[i]);          // past the row: -inf
+  }
+#pragma unroll
+  for (int i = 0; i < kSweeps; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (v[i][j] > -INFINITY) {
+        const double x = ((double)m - (double)v[i][j]) * invT;
+        const unsigned long long w = (unsigned long long)__double2ll_rn(exp64(-x, s.tbl) * unit);
+        const double b = x * per;
+        if (b < kFdSampleBins) atomicAdd(&s.mass[(int)b], w);
+        else tail += w;
+      }
+  unsigned long long all;
+  fd_block_scan<kWaves>(s, tail, all);
+  // thread t owns bins top - 2 t and the one below: sums from the far end
+  const int b0 = kFdSampleBins - 1 - 2 * t, b1 = b0 - 1;
+  const unsigned long long x0 = s.mass[b0], x1 = s.mass[b1];
+  unsigned long long ignore;
+  const unsigned long long before = fd_block_scan<kWaves>(s, x0 + x1, ignore) + all;
+  const double scale = (double)chunks / n / unit;
+  uint32_t low = 0, high = 0;                        // ~b of lo, b + 1 of hi
+  auto look = [&](int b, unsigned long long sum) {   // tokens from bin b on
+    const double M = scale * (double)sum, q = scale * unit * exp64(-b / per, s.tbl);
+    const double off = 4.0 * sqrt(q * M) + 8.0 * q;
+    if (M + off <= B) low = max(low, ~(uint32_t)b);
+    if (M - off >= B) high = max(high, (uint32_t)b + 1u);
+  };
+  look(b0, before + x0);
+  look(b1, before + x0 + x1);
+  low = fd_block_max<kWaves>(s, low);
+  high = fd_block_max<kWaves>(s, high);
+  if (low) lo = fmaxf(lo, (float)((double)m - T64 * ((double)~low / per)));
+  if (high) hi = (float)((double)m - T64 * ((double)(high - 1u) / per));
+}
+
+// One workgroup a row: the plan.
+template <typename T>
+__global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  FdShared& s = *reinterpret_cast<FdShared*>(dyn);
+  double* seg = reinterpret_cast<double*>(dyn + sizeof(FdShared));
+  constexpr int N = FdRow<T>::N, kWaves = kFdPlanThreads / kWave;
+  const int r = blockIdx.x, b = r / a.L, l = r % a.L, t = threadIdx.x;
+  const int lane = t % kWave, wave = t / kWave;
+  const float4* gmax = a.gmax + (size_t)r * a.nseg;
+  const double* ssum = a.ssum + (size_t)r * a.nseg;
+  const float u = a.tokens ? a.u[(size_t)b * a.usb + (size_t)l * a.usl] : 0.f;
+  const FdParams f = fd_params(a.f, b);
+  exp64_stage_table<kFdPlanThreads>(s.tbl);
+  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
+
+  // the row's largest logit; NaN or +inf anywhere shows as the largest key
+  uint32_t top = 0;
+  for (int g = t; g < a.nseg; g += kFdPlanThreads) {
+    const float4 x = gmax[g];
+    const float big = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+    const bool fine = x.x < INFINITY && x.y < INFINITY && x.z < INFINITY && x.w < INFINITY;
+    top = max(top, fine ? fkey(big) : 0xffffffffu);
+  }
+  top = fd_block_max<kWaves>(s, top);
+  const bool ok = f.ok && top > kNegInfKey && top != 0xffffffffu && u >= 0.f && u < 1.f;
+  const float m = ok ? unkey(top) : 0.f;
+  FdPlan plan = {kFdError, kFdDone, -1, m, -INFINITY, -INFINITY, INFINITY, -INFINITY, 0.0, 0.0, 0.0, 0.0};
   int y = -1;
   if (ok && f.T == 0.f) {
-    uint32_t best = 0xffffffffu;
-    fd_scan(row, [&](const float* v, int e) {
+    // the first group that reaches the maximum, and in it the first token
+    uint32_t first = 0;
+    for (int g = t; g < a.nseg; g += kFdPlanThreads) {
+      const uint32_t bits = fd_reach(gmax[g], m);
+      if (bits) first = max(first, ~(uint32_t)(g * kFdGroups + __ffs((int)bits) - 1));
+    }
+    first = ~fd_block_max<kWaves>(s, first);
+    if (wave == 0) {
+      float v[N];
+      const int q = (int)first * kWave + lane;
+      row.load(q, v);
+      int at = -1;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (v[i] == m) best = min(best, (uint32_t)(e + i));
-    });
-    y = (int)fd_block_min(s, best);
+      for (int i = N - 1; i >= 0; --i)
+        if (v[i] == m) at = row.first(q) + i;
+      y = lane_value(at, __ffsll((unsigned long long)__ballot(at >= 0)) - 1);
+    }
     plan.kind = kFdGreedy;
     plan.best = y;
   } else if (ok) {
-    const double invT = 1.0 / (double)f.T;
-    const int shift = 62 - (32 - __clz(a.V - 1 | 1));
-    const double unit = ldexp(1.0, shift);
-    auto fixed = [&](float z) {
-      return (unsigned long long)__double2ll_rn(fd_weight(z, m, invT, s.tbl) * unit);
-    };
-    const uint32_t top = fkey(m);
-    uint32_t low = kNegInfKey + 1;
-    if (f.k > 0 && f.k < a.V)
-      low = fd_search<false>(s, row, low, top, (double)f.k, [](float) { return 0ull; });
-    if (f.p < 1.f) {
-      unsigned long long sum = 0;
-      fd_scan(row, [&](const float* v, int) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (fkey(v[i]) >= low) sum += fixed(v[i]);
-      });
-      sum = fd_block_sum(s, sum);
-      low = fd_search<true>(s, row, low, top, (double)f.p * (double)sum, fixed);
-    }
-    float tau = low == kNegInfKey + 1 ? -INFINITY : unkey(low);
-    if (f.mp > 0.f) tau = fmaxf(tau, fd_min_p_threshold(m, invT, f.mp, s.tbl));
-
-    // kept mass of each segment, then of all before it
-    const int nv = row.vecs(), nseg = (nv + kFdSegVecs - 1) / kFdSegVecs;
-    for (int g = wave; g < nseg; g += kFdWaves) {
-      double w = 0.0;
-      for (int j = 0; j < kFdGroups; ++j) {
-        const int q = g * kFdSegVecs + j * kWave + lane;
-        if (q < nv) {
-          float v[N];
-          row.load(q, v);
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (v[i] >= tau) w += fd_weight(v[i], m, invT, s.tbl);
-        }
-      }
-      w = wave_sum(w);
-      if (lane == 0) s.seg[g] = w;
-    }
-    __syncthreads();
-    if (wave == 0) {
-      // lane l sums segments l per .. l per + per - 1
-      const int per = (nseg + kWave - 1) / kWave;
-      const int g0 = min(lane * per, nseg), g1 = min(g0 + per, nseg);
+    plan.kind = kFdDraw;
+    plan.invT = 1.0 / (double)f.T;
+    const bool by_k = f.k > 0 && f.k < a.V, by_p = f.p < 1.f;
+    if (fd_wants_sums(f, a.V)) {
       double mine = 0.0;
-      for (int g = g0; g < g1; ++g) mine += s.seg[g];
-      const double incl = wave_incl_scan(mine);
-      const double S = lane_value(incl, kWave - 1);
-      plan = {kFdDraw, -1, m, tau, invT, 1.0 / S};
-      if (a.tokens) {
-        const double t = (double)u * S;
-        // the first segment with weight whose running sum exceeds t, or where
-        // rounding leaves none the last with weight
-        double run = wave_shr1(incl), at = 0.0, last_at = 0.0;
-        int pick = -1, last = -1;
-        for (int g = g0; g < g1; ++g) {
-          const double w = s.seg[g];
-          if (w > 0.0) {
-            last = g;
-            last_at = run;
-            if (pick < 0 && run + w > t) {
-              pick = g;
-              at = run;
+      for (int g = t; g < a.nseg; g += kFdPlanThreads) {
+        const float4 x = gmax[g];
+        const float big = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+        const double w = big > -INFINITY ? ssum[g] * fd_weight(big, m, plan.invT, s.tbl) : 0.0;
+        seg[g] = w;
+        mine += w;
+      }
+      plan.Z = fd_block_sum<kWaves>(s, mine);
+    }
+    if (!by_k && !by_p && f.mp == 0.f) {
+      if (wave == 0) {
+        double S;
+        y = fd_draw(row, seg, a.nseg, a.tokens != nullptr, u, -INFINITY, m, plan.invT, s.tbl, S);
+        plan.invS = 1.0 / S;
+      }
+    } else {
+      if (f.mp > 0.f) plan.tau = fd_min_p_threshold(m, plan.invT, f.mp, s.tbl);
+      plan.need = by_k ? kFdTopK | (by_p ? kFdTopP : 0) : by_p ? kFdTopP : kFdSums;
+      if (by_k) {
+        // at least k tokens reach the k-th largest of the groups' maxima
+        if (f.k <= a.nseg * kFdGroups) {
+          auto maxima = [&](auto put) {
+            for (int g = t; g < a.nseg; g += kFdPlanThreads) {
+              const float4 x = gmax[g];
+              put(fd_key<T>(x.x), x.x);
+              put(fd_key<T>(x.y), x.y);
+              put(fd_key<T>(x.z), x.z);
+              put(fd_key<T>(x.w), x.w);
             }
-          }
-          run += w;
+          };
+          const FdFound k = fd_search<kFdPlanThreads, false, true>(
+              s, kFdLowest<T>, fd_key<T>(m), 0, (double)f.k, maxima, [](float) { return 0ull; });
+          if (k.reached) plan.lo = fd_unkey<T>(k.low);
         }
-        const uint64_t over = __ballot(pick >= 0), some = __ballot(last >= 0);
-        const int src = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)some);
-        const int seg = lane_value(over ? pick : last, src);
-        double base = lane_value(over ? at : last_at, src);
-        // inside it: the same over lanes, then over a lane's elements
-        int end = -1;
-        for (int j = 0; j < kFdGroups && y < 0; ++j) {
-          const int q = seg * kFdSegVecs + j * kWave + lane;
-          float v[N];
-          double w[N], sum = 0.0;
-          if (q < nv) row.load(q, v);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            w[i] = q < nv && v[i] >= tau ? fd_weight(v[i], m, invT, s.tbl) : 0.0;
-            sum += w[i];
-          }
-          const double in = wave_incl_scan(sum);
-          double run = base + wave_shr1(in);
-          int first = -1, tail = -1;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            run += w[i];
-            if (w[i] > 0.0) {
-              tail = row.first(q) + i;
-              if (first < 0 && run > t) first = tail;
-            }
-          }
-          const uint64_t hit = __ballot(first >= 0), any = __ballot(tail >= 0);
-          if (hit) y = lane_value(first, __ffsll((unsigned long long)hit) - 1);
-          if (any) end = lane_value(tail, 63 - __clzll((long long)any));
-          base += lane_value(in, kWave - 1);
+        // top-p is a part of the whole top-k set's mass
+        if (!by_p) plan.lo = fmaxf(plan.lo, plan.tau);
+      } else if (by_p) {
+        // Tokens below w hold less than V w: with V w = (1 - p) Z all that
+        // top-p keeps lies above w.  (Both sides with room for rounding.)
+        const double B = (1.0 - (double)f.p) * plan.Z, width = 1e-6 - log(B / a.V);
+        const double z = (double)m - (double)f.T * width;
+        const float bound = (float)(z - fabs(z) * 1e-6);
+        if (bound > -3e38f) plan.bound = bound;
+        plan.lo = plan.bound;
+        if (a.V > kFdSlot * 4 && width > 0.0) {
+          const double unit = ldexp(1.0, 62 - (32 - __clz((a.V - 1) | 1)));
+          fd_sample(s, row, m, plan.invT, (double)f.T, B, width, unit, plan.lo, plan.hi);
         }
-        if (y < 0) y = end;
+        // what min-p drops need not be looked at
+        plan.lo = fmaxf(plan.lo, plan.tau);
+        plan.hi = fmaxf(plan.hi, plan.lo);
+      } else {
+        plan.lo = plan.hi = plan.tau;
       }
     }
   }
-  if (threadIdx.x == 0) {
+  if (t == 0) {
     a.plans[r] = plan;
     if (a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
+  }
+}
+
+// One wave a segment that reaches the row's bracket.
+template <typename T>
+__global__ __launch_bounds__(kFdStatThreads) void filter_collect_kernel(FdArgs a, int nblk) {
+  constexpr int N = FdRow<T>::N;
+  __shared__ double tbl[SPECV_EXP64_N];
+  const int r = blockIdx.x / nblk, b = r / a.L, l = r % a.L;
+  const FdPlan* plan = a.plans + r;
+  if (plan->need == kFdDone) return;                 // uniform over the block
+  const int lane = threadIdx.x % kWave;
+  const int g = (blockIdx.x % nblk) * (kFdStatThreads / kWave) + threadIdx.x / kWave;
+  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
+  const float lo = plan->lo, hi = plan->hi, m = plan->m;
+  const uint32_t bits = g < a.nseg ? fd_reach(a.gmax[(size_t)r * a.nseg + g], lo) : 0u;
+  if (!__syncthreads_or(bits != 0u)) {
+    if (g < a.nseg && lane == 0) {
+      a.ssum[(size_t)r * a.nseg + g] = 0.0;
+      a.slot_n[(size_t)r * a.nseg + g] = 0u;
+    }
+    return;
+  }
+  float v[kFdGroups][N];
+  if (bits) fd_load(row, (uint32_t)g << 4 | bits, lane, v);
+  exp64_stage_table<kFdStatThreads>(tbl);
+  __syncthreads();
+  if (g >= a.nseg) return;
+  double w = 0.0;
+  uint32_t n = 0;
+  if (bits) {
+    const double invT = plan->invT;
+#pragma unroll
+    for (int j = 0; j < kFdGroups; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (v[j][i] >= hi) w += fd_weight(v[j][i], m, invT, tbl);
+        else if (v[j][i] >= lo && v[j][i] > -INFINITY) ++n;
+      }
+    w = wave_sum(w);
+    // in order of lanes: the same list at every run
+    const uint32_t incl = wave_incl_scan_u32(n);
+    uint32_t at = incl - n;
+    n = (uint32_t)lane_value((int)incl, kWave - 1);
+    if (n) {
+      float* slot = a.slots + ((size_t)r * a.nseg + g) * kFdSlot;
+#pragma unroll
+      for (int j = 0; j < kFdGroups; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (v[j][i] >= lo && v[j][i] < hi && v[j][i] > -INFINITY) {
+            if (at < (uint32_t)kFdSlot) slot[at] = v[j][i];
+            ++at;
+          }
+    }
+  }
+  if (lane == 0) {
+    a.ssum[(size_t)r * a.nseg + g] = w;
+    a.slot_n[(size_t)r * a.nseg + g] = n;
+  }
+}
+
+// One workgroup a row: its threshold and its draw.
+template <typename T>
+__global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  FdShared& s = *reinterpret_cast<FdShared*>(dyn);
+  double* seg = reinterpret_cast<double*>(dyn + sizeof(FdShared));
+  uint32_t* starts = reinterpret_cast<uint32_t*>(seg + a.nseg);      // or picks
+  float* list = reinterpret_cast<float*>(starts + a.nseg);
+  constexpr int N = FdRow<T>::N;
+  const int r = blockIdx.x, b = r / a.L, l = r % a.L, t = threadIdx.x;
+  const int lane = t % kWave, wave = t / kWave;
+  FdPlan plan = a.plans[r];
+  if (plan.need == kFdDone) return;
+  const float4* gmax = a.gmax + (size_t)r * a.nseg;
+  const double* ssum = a.ssum + (size_t)r * a.nseg;
+  const uint32_t* slot_n = a.slot_n + (size_t)r * a.nseg;
+  const float u = a.tokens ? a.u[(size_t)b * a.usb + (size_t)l * a.usl] : 0.f;
+  const FdParams f = fd_params(a.f, b);
+  if (t < SPECV_EXP64_N) s.tbl[t] = kExp64Table[t];
+  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
+  const double invT = plan.invT;
+  const float m = plan.m;
+  const double unit = ldexp(1.0, 62 - (32 - __clz((a.V - 1) | 1)));
+  auto fixed = [&](float z) {
+    return (unsigned long long)__double2ll_rn(fd_weight(z, m, invT, s.tbl) * unit);
+  };
+
+  // the collected logits, one list, in order
+  uint32_t n = 0;
+  bool whole = true;
+  double high = 0.0;
+  for (int g0 = 0; g0 < a.nseg; g0 += kFdThreads) {
+    const int g = g0 + t;
+    const uint32_t c = g < a.nseg ? slot_n[g] : 0u;
+    if (g < a.nseg) {
+      seg[g] = ssum[g];
+      high += seg[g];
+    }
+    whole = !__syncthreads_or(c > (uint32_t)kFdSlot) && whole;
+    unsigned long long total;
+    const uint32_t at = n + (uint32_t)fd_block_scan<kFdWaves>(s, c, total);
+    if (g < a.nseg) starts[g] = at;
+    n += (uint32_t)total;
+  }
+  whole = whole && n <= (uint32_t)a.list_cap;
+  high = fd_block_sum<kFdWaves>(s, high);
+  float tau = plan.tau;
+  if (whole) {
+    for (uint32_t e = t; e < n; e += kFdThreads) {
+      int g = 0;                                     // the last segment that starts at or before e
+      for (int step = 1 << 12; step; step >>= 1)
+        if (g + step < a.nseg && starts[g + step] <= e) g += step;
+      list[e] = a.slots[((size_t)r * a.nseg + g) * kFdSlot + (e - starts[g])];
+    }
+    __syncthreads();
+  }
+  if (plan.need & (kFdTopK | kFdTopP)) {
+    FdSource<T> src = {row, starts, 0u, list, n, true};
+    auto each = [&](auto put) { src.each([&](float z) { put(fd_key<T>(z), z); }); };
+    const uint32_t top = fd_key<T>(m);
+    auto search = [&](float from, unsigned long long above) -> FdFound {
+      FdFound k = {from > -INFINITY ? fd_key<T>(from) : kFdLowest<T>, true};
+      if (plan.need & kFdTopK)
+        k = fd_search<kFdThreads, false, false>(s, k.low, top, 0, (double)f.k, each,
+                                                [](float) { return 0ull; });
+      if (plan.need & kFdTopP) {
+        double target = (double)f.p * plan.Z * unit;
+        if (plan.need & kFdTopK) {
+          unsigned long long sum = 0, all;
+          each([&](uint32_t key, float z) {
+            if (key >= k.low) sum += fixed(z);
+          });
+          fd_block_scan<kFdWaves>(s, sum, all);
+          target = (double)f.p * (double)all;
+        }
+        k = fd_search<kFdThreads, true, false>(s, k.low, top, above, target, each, fixed);
+        k.reached = k.reached || (plan.need & kFdTopK);
+      }
+      return k;
+    };
+    FdFound k = {0u, false};
+    const double target = (double)f.p * plan.Z;
+    const bool only_p = !(plan.need & kFdTopK);
+    if (whole && !(only_p && high >= target)) {
+      k = search(plan.lo, (unsigned long long)__double2ll_rn(high * unit));
+      // not reached: the threshold lies below the bracket, and below min-p's if
+      // the bracket starts there
+      if (!k.reached) {
+        k.reached = plan.lo == plan.tau || !only_p;
+        k.low = plan.lo > -INFINITY ? fd_key<T>(plan.lo) : kFdLowest<T>;
+      }
+    }
+    if (!k.reached) {
+      // the sample misled, or a list is too short for it: all of the row that matters
+      const float from = only_p ? fmaxf(plan.bound, plan.tau) : plan.lo;
+      __syncthreads();
+      src.npick = fd_pick(s, starts, gmax, a.nseg, from);
+      src.listed = whole = false;
+      k = search(from, 0ull);
+    }
+    tau = fmaxf(tau, fd_unkey<T>(k.low));
+  } else if (!whole) {
+    whole = true;                                    // min-p alone collects nothing
+  }
+
+  // the kept mass of each segment
+  __syncthreads();
+  if (whole) {
+    if (n)
+      for (int g = wave; g < a.nseg; g += kFdWaves) {
+        const uint32_t from = starts[g], to = g + 1 < a.nseg ? starts[g + 1] : n;
+        if (from == to) continue;
+        double w = 0.0;
+        for (uint32_t e = from + lane; e < to; e += kWave)
+          if (list[e] >= tau) w += fd_weight(list[e], m, invT, s.tbl);
+        w = wave_sum(w);
+        if (lane == 0) seg[g] += w;
+      }
+  } else {
+    for (int g = t; g < a.nseg; g += kFdThreads) seg[g] = 0.0;
+    const uint32_t np = fd_pick(s, starts, gmax, a.nseg, tau);
+    for (uint32_t e = wave; e < np; e += kFdWaves) {
+      const uint32_t pick = starts[e];
+      float v[kFdGroups][N];
+      fd_load(row, pick, lane, v);
+      double w = 0.0;
+#pragma unroll
+      for (int j = 0; j < kFdGroups; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (v[j][i] >= tau && v[j][i] > -INFINITY) w += fd_weight(v[j][i], m, invT, s.tbl);
+      w = wave_sum(w);
+      if (lane == 0) seg[pick >> 4] = w;
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    double S;
+    const int y = fd_draw(row, seg, a.nseg, a.tokens != nullptr, u, tau, m, invT, s.tbl, S);
+    if (lane == 0) {
+      a.plans[r].tau = tau;
+      a.plans[r].invS = 1.0 / S;
+      if (a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
+    }
   }
 }
 
@@ -412,48 +884,127 @@ __device__ __forceinline__ float fd_prob(float z, double m, double c, float invS
 __device__ __forceinline__ void fd_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void fd_put(bf16_t* p, float v) { *p = bf16_bits(v); }
 
-// The probabilities: each thread one vector of logits.
-template <typename T, typename O>
-__global__ __launch_bounds__(256) void filter_probs_kernel(FdArgs a, int nblk) {
-  constexpr int N = FdRow<T>::N;
-  const int r = blockIdx.x / nblk, b = r / a.L, l = r % a.L;
-  const int q = (blockIdx.x % nblk) * 256 + threadIdx.x;
-  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
-  if (q >= row.vecs()) return;
-  const FdPlan p = a.plans[r];
-  O* out = static_cast<O*>(a.probs) + (size_t)b * a.psb + (size_t)l * a.psl;
-  const int e = row.first(q);
-  float v[N];
-  row.load(q, v);
-  const double c = p.invT * 1.4426950408889634, m = p.m;
+// The probabilities of one vector: whole 16- or 8-byte stores where the row's
+// place allows.
+template <typename O, int N>
+__device__ __forceinline__ void fd_put_all(O* out, int e, int V, const float (&w)[N]) {
+  constexpr int kBytes = N * (int)sizeof(O);
+  if (e >= 0 && e + N <= V && (reinterpret_cast<uintptr_t>(out + e) & (kBytes < 16 ? kBytes - 1 : 15)) == 0) {
+    uint32_t word[kBytes / 4];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float w = 0.f;
-    if (p.kind == kFdDraw && v[i] >= p.tau) w = fd_prob(v[i], m, c, (float)p.invS);
-    if (p.kind == kFdGreedy && e + i == p.best) w = 1.f;
-    if (e + i >= 0 && e + i < a.V) fd_put(out + e + i, w);
+    for (int i = 0; i < kBytes / 4; ++i)
+      word[i] = sizeof(O) == 4 ? __float_as_uint(w[i]) : bf16_pair(w[2 * i % N], w[(2 * i + 1) % N]);
+    if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2*>(out + e) = make_uint2(word[0], word[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        *(reinterpret_cast<uint4*>(out + e) + i) =
+            make_uint4(word[4 * i], word[4 * i + 1], word[4 * i + 2], word[4 * i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (e + i >= 0 && e + i < V) fd_put(out + e + i, w[i]);
   }
 }
 
-int fd_vecs(int V, bool bf16) { return bf16 ? (V + 7 + 7) / 8 : (V + 3 + 3) / 4; }
+// The probabilities: one wave a segment, which reads the groups that reach tau.
+template <typename T, typename O>
+__global__ __launch_bounds__(kFdStatThreads) void filter_probs_kernel(FdArgs a, int nblk) {
+  constexpr int N = FdRow<T>::N;
+  const int r = blockIdx.x / nblk, b = r / a.L, l = r % a.L, lane = threadIdx.x % kWave;
+  const int g = (blockIdx.x % nblk) * (kFdStatThreads / kWave) + threadIdx.x / kWave;
+  if (g >= a.nseg) return;
+  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
+  const FdPlan p = a.plans[r];
+  const float4 x = a.gmax[(size_t)r * a.nseg + g];
+  O* out = static_cast<O*>(a.probs) + (size_t)b * a.psb + (size_t)l * a.psl;
+  const double c = p.invT * 1.4426950408889634, m = p.m;
+  const bool draws = p.kind == kFdDraw;
+  const uint32_t bits = draws ? fd_reach(x, p.tau) : 0u;
+  float v[kFdGroups][N];
+  if (bits) fd_load(row, (uint32_t)g << 4 | bits, lane, v);
+#pragma unroll
+  for (int j = 0; j < kFdGroups; ++j) {
+    const int e = row.first(g * kFdSegVecs + j * kWave + lane);
+    float w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = 0.f;
+    if (bits >> j & 1u) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (v[j][i] >= p.tau) w[i] = fd_prob(v[j][i], m, c, (float)p.invS);
+    }
+    if (p.kind == kFdGreedy) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (e + i == p.best) w[i] = 1.f;
+    }
+    fd_put_all(out, e, a.V, w);
+  }
+}
+
+// Segments of the longest row of V logits: it may start inside a vector.
+int fd_segs(int V, bool bf16) {
+  const int n = bf16 ? 8 : 4;
+  return ((V + 2 * (n - 1)) / n + kFdSegVecs - 1) / kFdSegVecs;
+}
+int fd_blocks(int V, bool bf16) {
+  return (fd_segs(V, bf16) + kFdStatThreads / kWave - 1) / (kFdStatThreads / kWave);
+}
 
 bool filter_fits(int B, int L, int V, bool bf16) {
   const size_t rows = (size_t)B * L;
-  return grid_fits(rows, kFdThreads) && grid_fits(rows * ((fd_vecs(V, bf16) + 255) / 256), 256);
+  return grid_fits(rows, kFdThreads) && grid_fits(rows * fd_blocks(V, bf16), kFdStatThreads);
+}
+
+// Parts of the workspace, 16-byte aligned.
+struct FdLayout {
+  size_t gmax, ssum, slot_n, slots, bytes;
+};
+FdLayout fd_layout(size_t rows, int nseg) {
+  const size_t segs = (rows * nseg + 3) / 4 * 4;
+  FdLayout w;
+  w.gmax = rows * sizeof(FdPlan);
+  w.ssum = w.gmax + segs * sizeof(float4);
+  w.slot_n = w.ssum + segs * sizeof(double);
+  w.slots = w.slot_n + segs * sizeof(uint32_t);
+  w.bytes = w.slots + segs * kFdSlot * sizeof(float);
+  return w;
 }
 
 size_t filter_workspace_bytes(int B, int L, int V, bool bf16) {
-  return (size_t)B * L * sizeof(FdPlan);
+  return fd_layout((size_t)B * L, fd_segs(V, bf16)).bytes;
 }
 
+// LDS of the row kernel: the list takes what a CU has left, and no more than V.
+constexpr int kFdLds = 159 * 1024;                  // (the rest: the votes of __syncthreads_or)
+
 template <typename T>
-hipError_t fd_run(const FdArgs& a, size_t rows, bool probs_bf16, hipStream_t stream) {
-  filter_row_kernel<T><<<dim3((unsigned)rows), dim3(kFdThreads), 0, stream>>>(a);
+hipError_t fd_run(FdArgs a, size_t rows, bool probs_bf16, hipStream_t stream) {
+  const int nblk = fd_blocks(a.V, sizeof(T) == 2);
+  const dim3 grid((unsigned)(rows * nblk));
+  filter_stats_kernel<T><<<grid, dim3(kFdStatThreads), 0, stream>>>(a, nblk);
+  const int fixed = (int)sizeof(FdShared) + a.nseg * (int)(sizeof(double) + sizeof(uint32_t));
+  filter_plan_kernel<T><<<dim3((unsigned)rows), dim3(kFdPlanThreads), fixed, stream>>>(a);
+  // one setting for all rows that leaves nothing to collect ends here
+  const specv_filters_t& f = a.f;
+  const bool plain = !f.top_k_array && !f.top_p_array && !f.min_p_array &&
+                     (f.top_k == 0 || f.top_k >= a.V) && f.top_p == 1.f && f.min_p == 0.f;
+  const bool greedy = !f.temperature_array && f.temperature == 0.f;
+  if (!plain && !greedy) {
+    filter_collect_kernel<T><<<grid, dim3(kFdStatThreads), 0, stream>>>(a, nblk);
+    a.list_cap = min(a.V, (kFdLds - fixed) / (int)sizeof(float));
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(filter_row_kernel<T>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kFdLds);
+    if (e != hipSuccess) return e;
+    filter_row_kernel<T><<<dim3((unsigned)rows), dim3(kFdThreads),
+                           fixed + a.list_cap * (int)sizeof(float), stream>>>(a);
+  }
   if (a.probs) {
-    const int nblk = (fd_vecs(a.V, sizeof(T) == 2) + 255) / 256;
-    const dim3 grid((unsigned)(rows * nblk));
-    if (probs_bf16) filter_probs_kernel<T, bf16_t><<<grid, dim3(256), 0, stream>>>(a, nblk);
-    else filter_probs_kernel<T, float><<<grid, dim3(256), 0, stream>>>(a, nblk);
+    if (probs_bf16) filter_probs_kernel<T, bf16_t><<<grid, dim3(kFdStatThreads), 0, stream>>>(a, nblk);
+    else filter_probs_kernel<T, float><<<grid, dim3(kFdStatThreads), 0, stream>>>(a, nblk);
   }
   return hipGetLastError();
 }
@@ -463,9 +1014,16 @@ hipError_t launch_filter(const void* logits, long long zsb, long long zsl, bool 
                          long long usl, int* tokens, long long tsb, long long tsl, void* probs,
                          long long psb, long long psl, bool probs_bf16, void* workspace,
                          hipStream_t stream) {
-  const FdArgs a = {logits, zsb, zsl, L, V, f, u, usb, usl, tokens, tsb, tsl, probs, psb, psl,
-                    static_cast<FdPlan*>(workspace)};
+  FdArgs a = {logits, zsb, zsl, L, V, f, u, usb, usl, tokens, tsb, tsl, probs, psb, psl};
   const size_t rows = (size_t)B * L;
+  a.nseg = fd_segs(V, bf16);
+  const FdLayout w = fd_layout(rows, a.nseg);
+  char* base = static_cast<char*>(workspace);
+  a.plans = reinterpret_cast<FdPlan*>(base);
+  a.gmax = reinterpret_cast<float4*>(base + w.gmax);
+  a.ssum = reinterpret_cast<double*>(base + w.ssum);
+  a.slot_n = reinterpret_cast<uint32_t*>(base + w.slot_n);
+  a.slots = reinterpret_cast<float*>(base + w.slots);
   return bf16 ? fd_run<bf16_t>(a, rows, probs_bf16, stream)
               : fd_run<float>(a, rows, probs_bf16, stream);
 }
