@@ -152,7 +152,8 @@ typedef struct {
  *  probs       output, rows as of logits with its own strides, of probs_dtype
  *              (rounded to nearest even through float32), or NULL: tokens only.
  *  workspace   at least specv_filter_workspace_bytes(B, L, V, dtype) bytes,
- *              16-byte aligned; needs no initialisation.
+ *              16-byte aligned; needs no initialisation.  A small V needs none:
+ *              the size is then 0 (as for sizes the call refuses).
  *
  * B, L >= 1, 1 <= V <= SPECV_MAX_V.  Outputs and workspace do not overlap the
  * inputs or each other (between rows whose strides leave room they may lie),

@@ -165,7 +165,8 @@ specv_status_t specv_filter(const void* logits, int64_t stride_b, int64_t stride
       (probs && far(B, probs_stride_b, L, probs_stride_l, V)))
     return SPECV_EINVAL;
   const size_t need = filter_workspace_bytes(B, L, V, dtype == SPECV_BF16);
-  if (!workspace || misaligned(workspace, 16) || workspace_bytes < need) return SPECV_EWORKSPACE;
+  if (need > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
+    return SPECV_EWORKSPACE;
   const Rows z = {logits, stride_b * zs, stride_l * zs, B, L, V * zs};
   const Rows ur = {out_tokens ? u : nullptr, (size_t)u_stride_b * 4, (size_t)u_stride_l * 4, B, L, 4};
   const Rows t = {out_tokens, (size_t)token_stride_b * 4, (size_t)token_stride_l * 4, B, L, 4};

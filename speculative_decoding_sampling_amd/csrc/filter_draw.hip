@@ -103,15 +103,20 @@ struct FdRow {
   }
   __device__ __forceinline__ int vecs() const { return (V + off + N - 1) / N; }
   __device__ __forceinline__ int first(int q) const { return q * N - off; }
-  __device__ __forceinline__ void load(int q, float* out) const {
-    const int e = first(q);
-    if (e >= 0 && e + N <= V) {
-      load_vec_fast(p, e, out);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) out[i] = e + i >= 0 && e + i < V ? to_f32(p[e + i]) : -INFINITY;
-    }
+  __device__ __forceinline__ uint4 nothing() const {
+    const uint32_t x = N == 4 ? 0xff800000u : 0xff80ff80u;
+    return make_uint4(x, x, x, x);
   }
+  __device__ __forceinline__ uint4 raw(int q) const {
+    const int e = first(q);
+    if (e >= 0 && e + N <= V) return *reinterpret_cast<const uint4*>(p + e);
+    uint32_t x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = e + i >= 0 && e + i < V ? elem_bits(p, e + i) : neg_inf_bits(T{});
+    if constexpr (N == 4) return make_uint4(x[0], x[1], x[2], x[3]);
+    else return make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+  }
+  __device__ __forceinline__ void load(int q, float* out) const { unpack(raw(q), out, T{}); }
 };
 
 // The parameters of a request.
@@ -945,6 +950,243 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_probs_kernel(FdArgs a, 
   }
 }
 
+// The whole call for a short row: one workgroup, the row in LDS (each thread reads
+// its own vectors again, so without barriers), one read of the logits and no
+// workspace.
+//
+// For top-p the masses are sorted into bins of equal width in (m - z) / T, over the
+// range that holds all that top-p may keep: tokens that weigh less than (1 - p) /
+// V together hold less than (1 - p) of a mass that is at least 1.  One pass of
+// exponentials gives the total and the bin of the threshold; fd_search finds the
+// value in it.
+constexpr int kFdOneGroups = 144;                   // groups of 64 vectors
+constexpr int kFdOneV = 32768;
+
+struct FdOneShared {
+  FdShared s;
+  double group[kFdOneGroups];                       // their kept masses
+};
+static_assert(((kFdOneV + 6) / 4 + 63) / 64 <= kFdOneGroups, "every group has its mass");
+
+template <typename T, typename O>
+__global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
+  constexpr int N = FdRow<T>::N;
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  FdOneShared& o = *reinterpret_cast<FdOneShared*>(dyn);
+  FdShared& s = o.s;
+  uint4* kept = reinterpret_cast<uint4*>(dyn + (sizeof(FdOneShared) + 15) / 16 * 16);
+  const int r = blockIdx.x, b = r / a.L, l = r % a.L, t = threadIdx.x;
+  const int lane = t % kWave, wave = t / kWave;
+  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
+  const int nv = row.vecs();
+  const float u = a.tokens ? a.u[(size_t)b * a.usb + (size_t)l * a.usl] : 0.f;
+  const FdParams f = fd_params(a.f, b);
+  if (t < SPECV_EXP64_N) s.tbl[t] = kExp64Table[t];
+  float big = -INFINITY;
+  bool fine = true;
+#pragma unroll 4
+  for (int q = t; q < nv; q += kFdThreads) {
+    const uint4 raw = row.raw(q);
+    kept[q] = raw;
+    float v[N];
+    unpack(raw, v, T{});
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      big = fmaxf(big, v[j]);
+      fine = fine && v[j] < INFINITY;                // neither NaN nor +inf
+    }
+  }
+  const uint32_t top = fd_block_max<kFdWaves>(s, fine ? fkey(big) : 0xffffffffu);
+  const bool ok = f.ok && top > kNegInfKey && top != 0xffffffffu && u >= 0.f && u < 1.f;
+  const float m = ok ? unkey(top) : 0.f;
+  int y = -1;
+  float tau = INFINITY;
+  double invT = 0.0, invS = 0.0;
+  if (ok && f.T == 0.f) {
+    uint32_t first = 0;                              // ~ of the first id
+    for (int q = t; q < nv; q += kFdThreads) {
+      float v[N];
+      unpack(kept[q], v, T{});
+#pragma unroll
+      for (int j = N - 1; j >= 0; --j)
+        if (v[j] == m) first = max(first, ~(uint32_t)(row.first(q) + j));
+    }
+    y = (int)~fd_block_max<kFdWaves>(s, first);
+  } else if (ok) {
+    invT = 1.0 / (double)f.T;
+    const bool by_k = f.k > 0 && f.k < a.V, by_p = f.p < 1.f;
+    const double unit = ldexp(1.0, 62 - (32 - __clz((a.V - 1) | 1)));
+    auto fixed = [&](float z) {
+      return (unsigned long long)__double2ll_rn(fd_weight(z, m, invT, s.tbl) * unit);
+    };
+    auto each = [&](auto put) {
+      for (int q = t; q < nv; q += kFdThreads) {
+        float v[N];
+        unpack(kept[q], v, T{});
+#pragma unroll
+        for (int j = 0; j < N; ++j) put(fd_key<T>(v[j]), v[j]);
+      }
+    };
+    const uint32_t high = fd_key<T>(m);
+    tau = -INFINITY;
+    if (f.mp > 0.f) tau = fd_min_p_threshold(m, invT, f.mp, s.tbl);
+    uint32_t low = kFdLowest<T>;
+    if (by_k) {
+      if (f.k <= kFdThreads) {
+        // at least k tokens reach the k-th largest of the threads' maxima
+        const FdFound k = fd_search<kFdThreads, false, true>(
+            s, low, high, 0, (double)f.k, [&](auto put) { put(fd_key<T>(big), big); },
+            [](float) { return 0ull; });
+        if (k.reached) low = k.low;
+      }
+      low = fd_search<kFdThreads, false, false>(s, low, high, 0, (double)f.k, each,
+                                                [](float) { return 0ull; }).low;
+    }
+    if (by_p && by_k) {
+      unsigned long long sum = 0, all;
+      each([&](uint32_t key, float z) {
+        if (key >= low) sum += fixed(z);
+      });
+      fd_block_scan<kFdWaves>(s, sum, all);
+      low = fd_search<kFdThreads, true, false>(s, low, high, 0, (double)f.p * (double)all, each,
+                                               fixed).low;
+    } else if (by_p) {
+      const double width = 1e-6 - log((1.0 - (double)f.p) / a.V), per = kFdBins / width;
+      auto bin = [&](float z) { return ((double)m - (double)z) * invT * per; };
+      for (int i = t; i < kFdBins; i += kFdThreads) s.mass[i] = 0;
+      __syncthreads();
+      unsigned long long tail = 0, all, ignore;
+      each([&](uint32_t, float z) {
+        if (z > -INFINITY) {
+          const unsigned long long w = fixed(z);
+          const double x = bin(z);
+          if (x < kFdBins) atomicAdd(&s.mass[(int)x], w);
+          else tail += w;
+        }
+      });
+      __syncthreads();
+      const unsigned long long x0 = s.mass[2 * t], x1 = s.mass[2 * t + 1];
+      unsigned long long before = fd_block_scan<kFdWaves>(s, x0 + x1, all);
+      fd_block_scan<kFdWaves>(s, tail, ignore);
+      const double target = (double)f.p * (double)(all + ignore);
+      // the last bin that holds something and has less than the target before it
+      uint32_t mine = 0;
+      if (x0 && (double)before < target) mine = 2u * t + 1u;
+      if (x1 && (double)(before + x0) < target) mine = 2u * t + 2u;
+      const uint32_t found = fd_block_max<kFdWaves>(s, mine);
+      if (mine == found && found) s.above = found & 1u ? before : before + x0;
+      __syncthreads();
+      const int at = (int)found - 1;
+      // its values, with room for the edges' rounding; membership is by the bin
+      const double z1 = (double)m - (double)f.T * (at / per), z0 = (double)m - (double)f.T * ((at + 1) / per);
+      const double room = 1e-12 * (fabs((double)m) + fabs(z0) + fabs(z1));
+      const uint32_t k0 = fd_key<T>((float)(z0 - room)), k1 = fd_key<T>((float)(z1 + room));
+      low = fd_search<kFdThreads, true, false>(
+                s, max(kFdLowest<T>, k0 - min(k0, 1u)), min(high, k1 + 1u), s.above, target,
+                [&](auto put) {
+                  each([&](uint32_t key, float z) {
+                    const double x = bin(z);
+                    if (x >= at && x < at + 1) put(key, z);
+                  });
+                },
+                fixed).low;
+    }
+    if (by_k || by_p) tau = fmaxf(tau, fd_unkey<T>(low));
+
+    // kept mass of each group of 64 vectors
+    const int ngroup = (nv + kWave - 1) / kWave;
+    for (int g = wave; g < ngroup; g += kFdWaves) {
+      const int q = g * kWave + lane;
+      float v[N];
+      unpack(q < nv ? kept[q] : row.nothing(), v, T{});
+      double w = 0.0;
+      bool some = false;
+#pragma unroll
+      for (int j = 0; j < N; ++j) some = some || (v[j] >= tau && v[j] > -INFINITY);
+      if (__any(some)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (v[j] >= tau && v[j] > -INFINITY) w += fd_weight(v[j], m, invT, s.tbl);
+        w = wave_sum(w);
+      }
+      if (lane == 0) o.group[g] = w;
+    }
+    __syncthreads();
+    // every wave finds the group of the draw, the first draws
+    constexpr int kPer = (kFdOneGroups + kWave - 1) / kWave;
+    double w[kPer], mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      w[i] = lane * kPer + i < ngroup ? o.group[lane * kPer + i] : 0.0;
+      mine += w[i];
+    }
+    const double incl = wave_incl_scan(mine), S = lane_value(incl, kWave - 1);
+    invS = 1.0 / S;
+    if (a.tokens) {
+      const double target = (double)u * S;
+      double run = wave_shr1(incl), at = 0.0, last_at = 0.0;
+      int pick = -1, last = -1;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (w[i] > 0.0) {
+          last = lane * kPer + i;
+          last_at = run;
+          if (pick < 0 && run + w[i] > target) {
+            pick = last;
+            at = run;
+          }
+        }
+        run += w[i];
+      }
+      const uint64_t over = __ballot(pick >= 0), some = __ballot(last >= 0);
+      const int src = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)some);
+      const int g = lane_value(over ? pick : last, src);
+      const double base = lane_value(over ? at : last_at, src);
+      if (wave == 0) {
+        const int q = g * kWave + lane;
+        float v[N];
+        unpack(q < nv ? kept[q] : row.nothing(), v, T{});
+        double x[N], sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          x[j] = v[j] >= tau && v[j] > -INFINITY ? fd_weight(v[j], m, invT, s.tbl) : 0.0;
+          sum += x[j];
+        }
+        double here = base + wave_shr1(wave_incl_scan(sum));
+        int first = -1, tail = -1;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          here += x[j];
+          if (x[j] > 0.0) {
+            tail = row.first(q) + j;
+            if (first < 0 && here > target) first = tail;
+          }
+        }
+        const uint64_t hit = __ballot(first >= 0), any = __ballot(tail >= 0);
+        y = hit ? lane_value(first, __ffsll((unsigned long long)hit) - 1)
+                : lane_value(tail, 63 - __clzll((long long)any));
+      }
+    }
+  }
+  if (t == 0 && a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
+  if (a.probs) {
+    O* out = static_cast<O*>(a.probs) + (size_t)b * a.psb + (size_t)l * a.psl;
+    const double c = invT * 1.4426950408889634;
+    for (int q = t; q < nv; q += kFdThreads) {
+      const int e = row.first(q);
+      float v[N], w[N];
+      unpack(kept[q], v, T{});
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        w[j] = 0.f;
+        if (ok && v[j] >= tau) w[j] = fd_prob(v[j], m, c, (float)invS);
+        if (ok && f.T == 0.f) w[j] = e + j == y ? 1.f : 0.f;
+      }
+      fd_put_all(out, e, a.V, w);
+    }
+  }
+}
+
 // Segments of the longest row of V logits: it may start inside a vector.
 int fd_segs(int V, bool bf16) {
   const int n = bf16 ? 8 : 4;
@@ -975,6 +1217,7 @@ FdLayout fd_layout(size_t rows, int nseg) {
 }
 
 size_t filter_workspace_bytes(int B, int L, int V, bool bf16) {
+  if (V <= kFdOneV) return 0;
   return fd_layout((size_t)B * L, fd_segs(V, bf16)).bytes;
 }
 
@@ -983,6 +1226,16 @@ constexpr int kFdLds = 159 * 1024;                  // (the rest: the votes of _
 
 template <typename T>
 hipError_t fd_run(FdArgs a, size_t rows, bool probs_bf16, hipStream_t stream) {
+  if (a.V <= kFdOneV) {
+    const auto one = probs_bf16 ? filter_one_kernel<T, bf16_t> : filter_one_kernel<T, float>;
+    constexpr int N = Elem<T>::kPerVec;
+    const int lds = ((int)sizeof(FdOneShared) + 15) / 16 * 16 + (a.V + 2 * (N - 1)) / N * 16;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(one),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kFdLds);
+    if (e != hipSuccess) return e;
+    one<<<dim3((unsigned)rows), dim3(kFdThreads), lds, stream>>>(a);
+    return hipGetLastError();
+  }
   const int nblk = fd_blocks(a.V, sizeof(T) == 2);
   const dim3 grid((unsigned)(rows * nblk));
   filter_stats_kernel<T><<<grid, dim3(kFdStatThreads), 0, stream>>>(a, nblk);

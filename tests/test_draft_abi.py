@@ -90,8 +90,8 @@ def test_lm_head_refuses(lib):
 
 
 FILTER = ("z zsb zsl zt B L V f u usb usl out tsb tsl p psb psl pt ws wsb stream").split()
-FILTER_OK = dict(z=FAR[0], zsb=3 * 1000, zsl=1000, zt=0, B=4, L=3, V=1000, f={}, u=FAR[1], usb=3, usl=1,
-                 out=FAR[2], tsb=3, tsl=1, p=FAR[3], psb=3000, psl=1000, pt=0, ws=FAR[4], wsb=1 << 24,
+FILTER_OK = dict(z=FAR[0], zsb=3 * 40000, zsl=40000, zt=0, B=4, L=3, V=40000, f={}, u=FAR[1], usb=3, usl=1,
+                 out=FAR[2], tsb=3, tsl=1, p=FAR[3], psb=120000, psl=40000, pt=0, ws=FAR[4], wsb=1 << 28,
                  stream=None)
 
 
@@ -126,8 +126,8 @@ def test_filter_refuses(lib, kw):
     dict(ws=FAR[0]), dict(ws=FAR[3]), dict(ws=FAR[2]), dict(ws=FAR[1]),
     dict(f=dict(temperature_array=FAR[2])), dict(f=dict(top_p_array=FAR[3] + 16)),
     dict(f=dict(min_p_array=FAR[4])),
-    dict(psl=999), dict(psb=2999), dict(psb=0), dict(psl=0), dict(tsb=0), dict(tsl=0), dict(tsb=2),
-    dict(B=1, psl=500), dict(L=1, psb=999), dict(L=1, tsb=0),
+    dict(psl=39999), dict(psb=119999), dict(psb=0), dict(psl=0), dict(tsb=0), dict(tsl=0), dict(tsb=2),
+    dict(B=1, psl=500), dict(L=1, psb=39999), dict(L=1, tsb=0),
 ])
 def test_filter_refuses_outputs_that_overlap(lib, kw):
     assert call_filter(lib, **kw) == EINVAL
@@ -135,7 +135,8 @@ def test_filter_refuses_outputs_that_overlap(lib, kw):
 
 def test_filter_workspace_and_limits(lib):
     n = lib.specv_filter_workspace_bytes
-    assert n(4, 3, 1000, 0) > 0 and n(1, 1, 4194304, 1) > 0
+    assert n(4, 3, 40000, 0) > 0 and n(1, 1, 4194304, 1) > 0
+    assert n(4, 3, 1000, 0) == 0                                       # one kernel: none needed
     for a in ((0, 1, 10, 0), (1, 0, 10, 0), (1, 1, 0, 0), (1, 1, 4194305, 0), (1, 1, 10, 2)):
         assert n(*a) == 0
     for kw in (dict(ws=None), dict(ws=FAR[4] + 8), dict(wsb=16)):
@@ -147,8 +148,8 @@ def test_filter_workspace_and_limits(lib):
     # missing workspace is what is left to refuse
     assert call_filter(lib, p=None, pt=9, ws=None) == EWORKSPACE
     # transposed rows and rows in the gaps of others are fine: the same
-    assert call_filter(lib, tsb=1, tsl=4, psb=1000, psl=4000, ws=None) == EWORKSPACE
-    assert call_filter(lib, zsb=6000, zsl=2000, p=FAR[0] + 4000, psb=6000, psl=2000, ws=None) == EWORKSPACE
+    assert call_filter(lib, tsb=1, tsl=4, psb=40000, psl=160000, ws=None) == EWORKSPACE
+    assert call_filter(lib, zsb=240000, zsl=80000, p=FAR[0] + 160000, psb=240000, psl=80000, ws=None) == EWORKSPACE
 
 
 def test_python_calls_refuse_cpu_tensors(lib):

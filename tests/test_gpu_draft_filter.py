@@ -80,7 +80,7 @@ FILTERS = [(1.0, 0, 1.0, 0.0), (0.7, 50, 1.0, 0.0), (1.3, 0, 0.9, 0.0), (0.9, 0,
            (0.01, 0, 0.5, 0.0), (1.0, 0, 0.00001, 1.0), (100.0, 0, 0.3, 0.0), (1.0, 3000, 0.9, 0.0)]
 
 
-@pytest.mark.parametrize("V", [1, 2, 3, 7, 64, 100, 1000, 4097, 32000])
+@pytest.mark.parametrize("V", [1, 2, 3, 7, 64, 100, 1000, 4097, 32000, 32769, 50000])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_against_the_reference(V, dtype):
     R = 6
@@ -341,7 +341,8 @@ def test_python_refusals():
         with pytest.raises(S.SpecVerifyError):
             S.sample_filtered(z, u, **kw)
     with pytest.raises(S.SpecVerifyError) as e:
-        S.sample_filtered(z, u, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        S.sample_filtered(torch.zeros(3, 50000, device=DEV), u,
+                          workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert e.value.status == binding.SPECV_EWORKSPACE
     with pytest.raises(S.SpecVerifyError):
         S.sample_filtered(z[:0], u[:0])
