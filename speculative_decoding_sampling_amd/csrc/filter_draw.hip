@@ -12,10 +12,10 @@
 // less than p of the mass: both are a search, from the top, for the value at
 // which a running count or mass reaches a target.
 //
-// Numerics.  Weights are float64 (exp64).  A mass that decides tau_p is a sum of
-// whole multiples of 2^-s, s = 62 - ceil(log2 V): integer sums do not depend on
-// their order, so that the histograms may be built with atomics, and n tokens
-// are off by at most n 2^-(s+1) of the largest weight.  The sums of a draw are
+// Numerics.  Weights are float64.  A mass that decides tau_p is a sum of whole
+// multiples of 2^-s, s = 62 - ceil(log2 V) but at most 51: integer sums do not
+// depend on their order, so that the histograms may be built with atomics, and n
+// tokens are off by at most n 2^-(s+1) of the largest weight.  The sums of a draw are
 // float64 in a fixed order.
 //
 // Split.  A row is cut into groups, one 16-byte vector for each lane of a wave,
@@ -48,7 +48,7 @@ constexpr int kFdGroups = 4;                        // groups of a segment
 constexpr int kFdSegVecs = kFdGroups * kWave;       // 4 KB of logits
 constexpr int kFdStatThreads = 256;
 constexpr int kFdPlanThreads = 512;
-constexpr int kFdSlot = 256;                        // logits in the bracket that a segment can hold
+constexpr int kFdListCap = 16384;                   // collected logits of a row
 constexpr int kFdSampleBins = 2 * kFdPlanThreads;
 
 enum FdKind : int { kFdError = 0, kFdGreedy = 1, kFdDraw = 2 };
@@ -64,8 +64,9 @@ struct FdPlan {
                      // kernel: by min-p alone)
   float lo, hi;      // the bracket
   float bound;       // no token below it is kept by top-p
+  uint32_t listed;   // logits collected for the row
+  uint32_t pad;
   double invT, invS, Z;
-  double pad;
 };
 static_assert(sizeof(FdPlan) == 64, "FdPlan is 64 bytes");
 
@@ -84,9 +85,10 @@ struct FdArgs {
   float4* gmax;                     // [B L][nseg] largest logit of each group, NaN for a bad one
   double* ssum;                     // [B L][nseg] weights against the segment's largest logit, then
                                     // (collect) against the row's, from hi up
-  uint32_t* slot_n;                 // [B L][nseg] logits in the bracket
-  float* slots;                     // [B L][nseg][kFdSlot] those logits, in order
-  int nseg, list_cap;
+  uint2* part;                      // [B L][nseg] where a segment's logits of the bracket stand in
+                                    // the row's list, and how many they are
+  uint2* list;                      // [B L][cap] those logits, with their ids
+  int nseg, cap;
 };
 
 // A row as aligned 16-byte vectors.  The row may start inside the first one:
@@ -117,6 +119,11 @@ struct FdRow {
     else return make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
   }
   __device__ __forceinline__ void load(int q, float* out) const { unpack(raw(q), out, T{}); }
+  // Whether all of a segment's vectors lie in the row: its loads then need no
+  // bounds, each of which would part them.
+  __device__ __forceinline__ bool whole(int seg) const {
+    return first(seg * kFdSegVecs) >= 0 && first((seg + 1) * kFdSegVecs) <= V;
+  }
 };
 
 // The parameters of a request.
@@ -142,9 +149,36 @@ __device__ __forceinline__ bool fd_wants_sums(const FdParams& f, int V) {
   return f.ok && f.T > 0.f && (f.k == 0 || f.k >= V) && (f.p < 1.f || f.mp == 0.f);
 }
 
-// exp((z - m) / T), at most 1.
-__device__ __forceinline__ double fd_weight(float z, double m, double invT, const double* tbl) {
-  return exp64(((double)z - m) * invT, tbl);
+// Weights exp((z - m) / T), at most 1, by the table of exp64.h: with y = (z - m) N
+// / (T ln2), k = rint(y) and f = y - k in [-1/2, 1/2] the weight is 2^(k / N) 2^(f / N),
+// the second factor 1 + p(f).  Working in units of ln2 / N spares exp64's second
+// product; y's rounding costs |z - m| / T 2^-52 of the weight at most.
+struct FdExp {
+  double m, c;                                       // c = N / (T ln2)
+  const double* tbl;
+  __device__ __forceinline__ FdExp(double m, double invT, const double* tbl)
+      : m(m), c(invT * SPECV_EXP64_INV_L), tbl(tbl) {}
+  __device__ __forceinline__ double units(float z) const { return ((double)z - m) * c; }
+  __device__ __forceinline__ double of_units(double y) const {
+    y = fmax(y, -551000.0);                          // below e^-745: 0
+    const double t = y + SPECV_EXP64_SHIFT, f = y - (t - SPECV_EXP64_SHIFT);
+    const int k = (int)(unsigned)__double_as_longlong(t);
+    constexpr double L = SPECV_EXP64_L;
+    double q = fma(f, L * L * L / 6, L * L / 2);
+    q = fma(f, q, L);
+    const double tj = tbl[k & (SPECV_EXP64_N - 1)];
+    return ldexp(fma(tj, q * f, tj), k >> SPECV_EXP64_LOG2N);
+  }
+  __device__ __forceinline__ double operator()(float z) const { return of_units(units(z)); }
+};
+
+// Weights as whole multiples of 2^-s: the sum with 2^52 leaves them in its low
+// bits, rounded to nearest.
+__device__ __forceinline__ double fd_unit(int V) {
+  return __hiloint2double((1023 + min(62 - (32 - __clz((V - 1) | 1)), 51)) << 20, 0);
+}
+__device__ __forceinline__ unsigned long long fd_fixed(double w, double unit) {
+  return (unsigned long long)__double_as_longlong(fma(w, unit, 4503599627370496.0)) & 0xfffffffffffffull;
 }
 
 // A row's groups: one wave a segment.
@@ -154,13 +188,20 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_stats_kernel(FdArgs a, 
   __shared__ double tbl[SPECV_EXP64_N];
   const int r = blockIdx.x / nblk, b = r / a.L, l = r % a.L;
   const int lane = threadIdx.x % kWave;
-  const int g = (blockIdx.x % nblk) * (kFdStatThreads / kWave) + threadIdx.x / kWave;
+  const int g = (blockIdx.x % nblk) * (kFdStatThreads / kWave) +
+                __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
+  uint4 raw[kFdGroups];
+  if (row.whole(g)) {
+#pragma unroll
+    for (int j = 0; j < kFdGroups; ++j)
+      raw[j] = *reinterpret_cast<const uint4*>(row.p + row.first(g * kFdSegVecs + j * kWave + lane));
+  } else {
+#pragma unroll
+    for (int j = 0; j < kFdGroups; ++j) raw[j] = row.raw(g * kFdSegVecs + j * kWave + lane);
+  }
   const FdParams f = fd_params(a.f, b);
   const bool sums = fd_wants_sums(f, a.V);
-  float v[kFdGroups][N];
-#pragma unroll
-  for (int j = 0; j < kFdGroups; ++j) row.load(g * kFdSegVecs + j * kWave + lane, v[j]);
   if (sums) {
     exp64_stage_table<kFdStatThreads>(tbl);
     __syncthreads();
@@ -169,24 +210,29 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_stats_kernel(FdArgs a, 
   float top[kFdGroups], m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < kFdGroups; ++j) {
-    bool bad = false;
+    float v[N];
+    unpack(raw[j], v, T{});
+    bool fine = true;
     top[j] = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      top[j] = fmaxf(top[j], v[j][i]);
-      bad = bad || !(v[j][i] < INFINITY);            // NaN or +inf
+      top[j] = fmaxf(top[j], v[i]);
+      fine = fine && v[i] < INFINITY;                // neither NaN nor +inf
     }
     top[j] = wave_max(top[j]);
     m = fmaxf(m, top[j]);
-    if (__any(bad)) top[j] = __builtin_nanf("");
+    if (!__all(fine)) top[j] = __builtin_nanf("");
   }
   double w = 0.0;
   if (sums && m > -INFINITY) {
-    const double invT = 1.0 / (double)f.T;
+    const FdExp e(m, 1.0 / (double)f.T, tbl);
 #pragma unroll
-    for (int j = 0; j < kFdGroups; ++j)
+    for (int j = 0; j < kFdGroups; ++j) {
+      float v[N];
+      unpack(raw[j], v, T{});
 #pragma unroll
-      for (int i = 0; i < N; ++i) w += fd_weight(v[j][i], m, invT, tbl);
+      for (int i = 0; i < N; ++i) w += e(v[i]);
+    }
     w = wave_sum(w);
   }
   if (lane == 0) {
@@ -203,6 +249,7 @@ struct FdShared {
   uint32_t count[kFdBins];
   unsigned long long wave_u64[kFdWaves];
   uint32_t wave_u32[kFdWaves];
+  int found[2 * kFdGroups];
   uint32_t npick;
   unsigned long long above;
 };
@@ -406,19 +453,24 @@ __device__ __forceinline__ FdFound fd_search(FdShared& s, uint32_t lo, uint32_t 
 }
 
 // The smallest float whose weight is at least mp, in (0, 1]: a search over keys
-// in which each lane of a wave tries one of 64 (6 rounds for 32 bits).
-__device__ __forceinline__ float fd_min_p_threshold(float m, double invT, float mp,
-                                                    const double* tbl) {
+// in which each lane of a wave tries one of 64, first those around m + T log mp,
+// then, where that is too far off, of all (6 rounds for 32 bits).
+__device__ __forceinline__ float fd_min_p_threshold(float m, float T, const FdExp& e, float mp) {
   const int lane = threadIdx.x % kWave;
   uint32_t lo = kNegInfKey + 1, hi = fkey(m);        // the maximum itself has weight 1
+  auto weighs = [&](uint32_t key) { return e(unkey(key)) >= (double)mp; };
+  const uint32_t guess = fkey((float)fmax((double)m + (double)T * log((double)mp), -3e38));
+  const uint32_t near = min(max(guess + lane - 32u, lo), hi);
+  const uint64_t yes = __ballot(weighs(near));
+  if (yes != 0 && !(yes & 1ull)) return unkey((uint32_t)lane_value((int)near, __ffsll((unsigned long long)yes) - 1));
   while (lo < hi) {
     const uint32_t step = (hi - lo) / kWave + 1;
     auto key = [&](int i) { return lo + min((uint32_t)i * step, hi - lo); };
-    const uint64_t yes = __ballot(fd_weight(unkey(key(lane)), m, invT, tbl) >= (double)mp);
-    if (yes == 0) {
+    const uint64_t some = __ballot(weighs(key(lane)));
+    if (some == 0) {
       lo = key(kWave - 1) + 1;
     } else {
-      const int i = __ffsll((unsigned long long)yes) - 1;
+      const int i = __ffsll((unsigned long long)some) - 1;
       hi = key(i);
       if (i > 0) lo = key(i - 1) + 1;
     }
@@ -426,15 +478,72 @@ __device__ __forceinline__ float fd_min_p_threshold(float m, double invT, float 
   return unkey(hi);
 }
 
-// The draw from a row's segment masses seg (in LDS), by one wave: S their sum,
-// and where a token is wanted the first whose running sum exceeds u S, or where
-// rounding leaves none the last with weight.
+// A short list's threshold and draw, by one wave without barriers: lane i holds
+// entry i of n.  The entries are all the tokens that top-k and top-p are about
+// (want_k, want_p: the filters that are on; target: top-p's, where top-k is off).
+struct FdShort {
+  bool reached;      // top-p's target, with the whole list
+  bool kept;         // this lane's entry
+};
+__device__ __forceinline__ FdShort fd_short(uint32_t key, unsigned long long mass, int n, bool want_k,
+                                            int k, bool want_p, double p, double target) {
+  const int lane = threadIdx.x % kWave;
+  FdShort r = {true, lane < n};
+  if (want_k) {
+    int above = 0;
+    for (int j = 0; j < n; ++j) above += (uint32_t)lane_value((int)key, j) > key ? 1 : 0;
+    r.kept = r.kept && above < k;
+  }
+  if (want_p) {
+    const unsigned long long mine = r.kept ? mass : 0ull;
+    const int lo = (int)(uint32_t)mine, hi = (int)(uint32_t)(mine >> 32);
+    unsigned long long above = 0, all = 0;
+    for (int j = 0; j < n; ++j) {
+      const unsigned long long w =
+          (unsigned long long)(uint32_t)lane_value(hi, j) << 32 | (uint32_t)lane_value(lo, j);
+      all += w;
+      above += (uint32_t)lane_value((int)key, j) > key ? w : 0ull;
+    }
+    if (want_k) target = p * (double)all;
+    r.reached = (double)all >= target;
+    r.kept = r.kept && (double)above < target;
+  }
+  return r;
+}
+// The token drawn at u from the kept entries in order of their ids (their sum in
+// S), -1 where none is wanted.
+__device__ __forceinline__ int fd_short_draw(bool kept, int id, double w, int n, bool token, float u,
+                                             double& S) {
+  const int lane = threadIdx.x % kWave;
+  const uint64_t in = __ballot(kept);
+  const uint32_t mine = kept ? (uint32_t)id : 0xffffffffu;
+  int rank = 0;
+  for (int j = 0; j < n; ++j) rank += (uint32_t)lane_value((int)mine, j) < mine ? 1 : 0;
+  // the others behind them: every lane's entry moves to a lane of its own
+  if (!kept) rank = __popcll(in) + __popcll(~in & ((1ull << lane) - 1ull));
+  w = kept ? w : 0.0;
+  const int lo = __builtin_amdgcn_ds_permute(rank * 4, __double2loint(w));
+  const int hi = __builtin_amdgcn_ds_permute(rank * 4, __double2hiint(w));
+  id = __builtin_amdgcn_ds_permute(rank * 4, id);
+  w = __hiloint2double(hi, lo);
+  const double incl = wave_incl_scan(w);
+  S = lane_value(incl, kWave - 1);
+  if (!token) return -1;
+  const uint64_t over = __ballot(w > 0.0 && incl > (double)u * S), some = __ballot(w > 0.0);
+  return lane_value(id, over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)some));
+}
+
+// The draw from a row's segment masses seg (in LDS), by the whole block: S their
+// sum, and where a token is wanted the first whose running sum exceeds u S, or
+// where rounding leaves none the last with weight.  Every wave finds the segment;
+// the first four take one of its groups each.
 template <typename T>
-__device__ __forceinline__ int fd_draw(const FdRow<T>& row, const double* seg, int nseg, bool token,
-                                       float u, float tau, float m, double invT, const double* tbl,
+__device__ __forceinline__ int fd_draw(FdShared& s, const FdRow<T>& row, const double* seg, int nseg,
+                                       bool token, float u, float tau, const FdExp& weight,
                                        double& S) {
   constexpr int N = FdRow<T>::N;
   const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   // lane l sums segments l per .. l per + per - 1
   const int per = (nseg + kWave - 1) / kWave;
   const int g0 = min(lane * per, nseg), g1 = min(g0 + per, nseg);
@@ -461,22 +570,26 @@ __device__ __forceinline__ int fd_draw(const FdRow<T>& row, const double* seg, i
   const uint64_t over = __ballot(pick >= 0), some = __ballot(last >= 0);
   const int src = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)some);
   const int g = lane_value(over ? pick : last, src);
-  double base = lane_value(over ? at : last_at, src);
-  // inside it: the same over lanes, then over a lane's elements
-  float v[kFdGroups][N];
-  fd_load(row, (uint32_t)g << 4 | 15u, lane, v);
-  int y = -1, end = -1;
-#pragma unroll
-  for (int j = 0; j < kFdGroups; ++j) {
-    const int e = row.first(g * kFdSegVecs + j * kWave + lane);
-    double w[N], sum = 0.0;
+  const double base = lane_value(over ? at : last_at, src);
+  // inside it: sums of the groups, then over lanes, then over a lane's elements
+  const int q = g * kFdSegVecs + wave * kWave + lane, e = row.first(q);
+  double w[N], sum = 0.0;
+  if (wave < kFdGroups) {
+    float v[N];
+    row.load(q, v);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      w[i] = v[j][i] >= tau && v[j][i] > -INFINITY ? fd_weight(v[j][i], m, invT, tbl) : 0.0;
+      w[i] = v[i] >= tau && v[i] > -INFINITY ? weight(v[i]) : 0.0;
       sum += w[i];
     }
-    const double in = wave_incl_scan(sum);
-    double here = base + wave_shr1(in);
+    sum = wave_incl_scan(sum);
+    if (lane == kWave - 1) s.wave_u64[wave] = __double_as_longlong(sum);
+  }
+  __syncthreads();
+  if (wave < kFdGroups) {
+    double here = base;
+    for (int i = 0; i < wave; ++i) here += __longlong_as_double(s.wave_u64[i]);
+    here += wave_shr1(sum);
     int first = -1, tail = -1;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -487,9 +600,17 @@ __device__ __forceinline__ int fd_draw(const FdRow<T>& row, const double* seg, i
       }
     }
     const uint64_t hit = __ballot(first >= 0), any = __ballot(tail >= 0);
-    if (hit && y < 0) y = lane_value(first, __ffsll((unsigned long long)hit) - 1);
-    if (any) end = lane_value(tail, 63 - __clzll((long long)any));
-    base += lane_value(in, kWave - 1);
+    if (lane == 0) {
+      s.found[wave] = hit ? lane_value(first, __ffsll((unsigned long long)hit) - 1) : -1;
+      s.found[kFdGroups + wave] = any ? lane_value(tail, 63 - __clzll((long long)any)) : -1;
+    }
+  }
+  __syncthreads();
+  int y = -1, end = -1;
+#pragma unroll
+  for (int i = 0; i < kFdGroups; ++i) {
+    if (y < 0) y = s.found[i];
+    if (s.found[kFdGroups + i] >= 0) end = s.found[kFdGroups + i];
   }
   return y < 0 ? end : y;
 }
@@ -502,7 +623,7 @@ __device__ __forceinline__ int fd_draw(const FdRow<T>& row, const double* seg, i
 // four deviations and eight tokens are below B, hi the lowest at which M less
 // those is above it.  Nothing rests on it but the time: the row kernel checks.
 template <typename T>
-__device__ __forceinline__ void fd_sample(FdShared& s, const FdRow<T>& row, float m, double invT,
+__device__ __forceinline__ void fd_sample(FdShared& s, const FdRow<T>& row, const FdExp& weight,
                                           double T64, double B, double width, double unit, float& lo,
                                           float& hi) {
   constexpr int N = FdRow<T>::N, kChunk = 16, kWaves = kFdPlanThreads / kWave;
@@ -511,7 +632,7 @@ __device__ __forceinline__ void fd_sample(FdShared& s, const FdRow<T>& row, floa
   const int n = min(chunks, kChunks);
   for (int i = t; i < kFdSampleBins; i += kFdPlanThreads) s.mass[i] = 0;
   __syncthreads();
-  const double per = kFdSampleBins / width;
+  const double per = kFdSampleBins / width, bins = per / SPECV_EXP64_INV_L;
   unsigned long long tail = 0;
   constexpr int kSweeps = kChunks * kChunk / kFdPlanThreads;
   float v[kSweeps][N];
@@ -526,9 +647,9 @@ __device__ __forceinline__ void fd_sample(FdShared& s, const FdRow<T>& row, floa
 #pragma unroll
     for (int j = 0; j < N; ++j)
       if (v[i][j] > -INFINITY) {
-        const double x = ((double)m - (double)v[i][j]) * invT;
-        const unsigned long long w = (unsigned long long)__double2ll_rn(exp64(-x, s.tbl) * unit);
-        const double b = x * per;
+        const double x = weight.units(v[i][j]);
+        const unsigned long long w = fd_fixed(weight.of_units(x), unit);
+        const double b = -x * bins;
         if (b < kFdSampleBins) atomicAdd(&s.mass[(int)b], w);
         else tail += w;
       }
@@ -551,8 +672,8 @@ __device__ __forceinline__ void fd_sample(FdShared& s, const FdRow<T>& row, floa
   look(b1, before + x0 + x1);
   low = fd_block_max<kWaves>(s, low);
   high = fd_block_max<kWaves>(s, high);
-  if (low) lo = fmaxf(lo, (float)((double)m - T64 * ((double)~low / per)));
-  if (high) hi = (float)((double)m - T64 * ((double)(high - 1u) / per));
+  if (low) lo = fmaxf(lo, (float)(weight.m - T64 * ((double)~low / per)));
+  if (high) hi = (float)(weight.m - T64 * ((double)(high - 1u) / per));
 }
 
 // One workgroup a row: the plan.
@@ -582,7 +703,7 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
   top = fd_block_max<kWaves>(s, top);
   const bool ok = f.ok && top > kNegInfKey && top != 0xffffffffu && u >= 0.f && u < 1.f;
   const float m = ok ? unkey(top) : 0.f;
-  FdPlan plan = {kFdError, kFdDone, -1, m, -INFINITY, -INFINITY, INFINITY, -INFINITY, 0.0, 0.0, 0.0, 0.0};
+  FdPlan plan = {kFdError, kFdDone, -1, m, -INFINITY, -INFINITY, INFINITY, -INFINITY, 0u, 0u, 0.0, 0.0, 0.0};
   int y = -1;
   if (ok && f.T == 0.f) {
     // the first group that reaches the maximum, and in it the first token
@@ -607,26 +728,25 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
   } else if (ok) {
     plan.kind = kFdDraw;
     plan.invT = 1.0 / (double)f.T;
+    const FdExp weight(m, plan.invT, s.tbl);
     const bool by_k = f.k > 0 && f.k < a.V, by_p = f.p < 1.f;
     if (fd_wants_sums(f, a.V)) {
       double mine = 0.0;
       for (int g = t; g < a.nseg; g += kFdPlanThreads) {
         const float4 x = gmax[g];
         const float big = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
-        const double w = big > -INFINITY ? ssum[g] * fd_weight(big, m, plan.invT, s.tbl) : 0.0;
+        const double w = big > -INFINITY ? ssum[g] * weight(big) : 0.0;
         seg[g] = w;
         mine += w;
       }
       plan.Z = fd_block_sum<kWaves>(s, mine);
     }
     if (!by_k && !by_p && f.mp == 0.f) {
-      if (wave == 0) {
-        double S;
-        y = fd_draw(row, seg, a.nseg, a.tokens != nullptr, u, -INFINITY, m, plan.invT, s.tbl, S);
-        plan.invS = 1.0 / S;
-      }
+      double S;
+      y = fd_draw(s, row, seg, a.nseg, a.tokens != nullptr, u, -INFINITY, weight, S);
+      plan.invS = 1.0 / S;
     } else {
-      if (f.mp > 0.f) plan.tau = fd_min_p_threshold(m, plan.invT, f.mp, s.tbl);
+      if (f.mp > 0.f) plan.tau = fd_min_p_threshold(m, f.T, weight, f.mp);
       plan.need = by_k ? kFdTopK | (by_p ? kFdTopP : 0) : by_p ? kFdTopP : kFdSums;
       if (by_k) {
         // at least k tokens reach the k-th largest of the groups' maxima
@@ -654,10 +774,8 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
         const float bound = (float)(z - fabs(z) * 1e-6);
         if (bound > -3e38f) plan.bound = bound;
         plan.lo = plan.bound;
-        if (a.V > kFdSlot * 4 && width > 0.0) {
-          const double unit = ldexp(1.0, 62 - (32 - __clz((a.V - 1) | 1)));
-          fd_sample(s, row, m, plan.invT, (double)f.T, B, width, unit, plan.lo, plan.hi);
-        }
+        if (width > 0.0)
+          fd_sample(s, row, weight, (double)f.T, B, width, fd_unit(a.V), plan.lo, plan.hi);
         // what min-p drops need not be looked at
         plan.lo = fmaxf(plan.lo, plan.tau);
         plan.hi = fmaxf(plan.hi, plan.lo);
@@ -678,56 +796,69 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_collect_kernel(FdArgs a
   constexpr int N = FdRow<T>::N;
   __shared__ double tbl[SPECV_EXP64_N];
   const int r = blockIdx.x / nblk, b = r / a.L, l = r % a.L;
-  const FdPlan* plan = a.plans + r;
-  if (plan->need == kFdDone) return;                 // uniform over the block
   const int lane = threadIdx.x % kWave;
-  const int g = (blockIdx.x % nblk) * (kFdStatThreads / kWave) + threadIdx.x / kWave;
-  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
+  const int g = (blockIdx.x % nblk) * (kFdStatThreads / kWave) +
+                __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const size_t at = (size_t)r * a.nseg + g;
+  FdPlan* plan = a.plans + r;
+  Exp64Stage<kFdStatThreads> stage;
+  stage.fetch();
+  const float4 gm = g < a.nseg ? a.gmax[at] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
   const float lo = plan->lo, hi = plan->hi, m = plan->m;
-  const uint32_t bits = g < a.nseg ? fd_reach(a.gmax[(size_t)r * a.nseg + g], lo) : 0u;
-  if (!__syncthreads_or(bits != 0u)) {
-    if (g < a.nseg && lane == 0) {
-      a.ssum[(size_t)r * a.nseg + g] = 0.0;
-      a.slot_n[(size_t)r * a.nseg + g] = 0u;
-    }
-    return;
-  }
+  const double invT = plan->invT;
+  if (plan->need == kFdDone) return;                 // uniform over the block
+  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
+  const uint32_t bits = gm.x > -INFINITY || gm.y > -INFINITY || gm.z > -INFINITY || gm.w > -INFINITY
+                            ? fd_reach(gm, lo) : 0u;
+  // weights from hi up
+  const bool sums = gm.x >= hi || gm.y >= hi || gm.z >= hi || gm.w >= hi;
   float v[kFdGroups][N];
   if (bits) fd_load(row, (uint32_t)g << 4 | bits, lane, v);
-  exp64_stage_table<kFdStatThreads>(tbl);
-  __syncthreads();
+  if (__syncthreads_or(sums)) {
+    stage.store(tbl);
+    __syncthreads();
+  }
   if (g >= a.nseg) return;
   double w = 0.0;
-  uint32_t n = 0;
+  uint32_t n = 0, from = 0;
   if (bits) {
-    const double invT = plan->invT;
+    if (sums) {
+      const FdExp weight(m, invT, tbl);
+#pragma unroll
+      for (int j = 0; j < kFdGroups; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (v[j][i] >= hi) w += weight(v[j][i]);
+      w = wave_sum(w);
+    }
 #pragma unroll
     for (int j = 0; j < kFdGroups; ++j)
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (v[j][i] >= hi) w += fd_weight(v[j][i], m, invT, tbl);
-        else if (v[j][i] >= lo && v[j][i] > -INFINITY) ++n;
-      }
-    w = wave_sum(w);
-    // in order of lanes: the same list at every run
+      for (int i = 0; i < N; ++i) n += v[j][i] >= lo && v[j][i] < hi && v[j][i] > -INFINITY ? 1u : 0u;
     const uint32_t incl = wave_incl_scan_u32(n);
-    uint32_t at = incl - n;
+    uint32_t mine = incl - n;
     n = (uint32_t)lane_value((int)incl, kWave - 1);
     if (n) {
-      float* slot = a.slots + ((size_t)r * a.nseg + g) * kFdSlot;
+      // a piece of the row's list, its entries in order of lanes
+      if (lane == 0) from = atomicAdd(&plan->listed, n);
+      from = (uint32_t)lane_value((int)from, 0);
+      uint2* list = a.list + (size_t)r * a.cap;
+      mine += from;
 #pragma unroll
       for (int j = 0; j < kFdGroups; ++j)
 #pragma unroll
         for (int i = 0; i < N; ++i)
           if (v[j][i] >= lo && v[j][i] < hi && v[j][i] > -INFINITY) {
-            if (at < (uint32_t)kFdSlot) slot[at] = v[j][i];
-            ++at;
+            if (mine < (uint32_t)a.cap)
+              list[mine] = make_uint2(__float_as_uint(v[j][i]),
+                                      (uint32_t)(row.first(g * kFdSegVecs + j * kWave + lane) + i));
+            ++mine;
           }
     }
   }
   if (lane == 0) {
-    a.ssum[(size_t)r * a.nseg + g] = w;
-    a.slot_n[(size_t)r * a.nseg + g] = n;
+    a.ssum[at] = w;
+    a.part[at] = make_uint2(from, n);
   }
 }
 
@@ -737,68 +868,73 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   FdShared& s = *reinterpret_cast<FdShared*>(dyn);
   double* seg = reinterpret_cast<double*>(dyn + sizeof(FdShared));
-  uint32_t* starts = reinterpret_cast<uint32_t*>(seg + a.nseg);      // or picks
-  float* list = reinterpret_cast<float*>(starts + a.nseg);
+  uint32_t* picks = reinterpret_cast<uint32_t*>(seg + a.nseg);
+  float* list = reinterpret_cast<float*>(picks + a.nseg);
   constexpr int N = FdRow<T>::N;
   const int r = blockIdx.x, b = r / a.L, l = r % a.L, t = threadIdx.x;
-  const int lane = t % kWave, wave = t / kWave;
-  FdPlan plan = a.plans[r];
-  if (plan.need == kFdDone) return;
-  const float4* gmax = a.gmax + (size_t)r * a.nseg;
-  const double* ssum = a.ssum + (size_t)r * a.nseg;
-  const uint32_t* slot_n = a.slot_n + (size_t)r * a.nseg;
+  const int lane = t % kWave, wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const FdPlan plan = a.plans[r];
+  const uint2* found = a.list + (size_t)r * a.cap;
+  uint2 entry = make_uint2(0u, 0u);
+  if (lane < a.cap) entry = found[lane];             // (what stands there, if not enough was collected)
   const float u = a.tokens ? a.u[(size_t)b * a.usb + (size_t)l * a.usl] : 0.f;
   const FdParams f = fd_params(a.f, b);
+  if (plan.need == kFdDone) return;
+  const bool by_k = plan.need & kFdTopK, by_p = plan.need & kFdTopP;
+  const uint32_t n = plan.listed;
+  const float m = plan.m;
+  const double invT = plan.invT, unit = fd_unit(a.V);
+  float tau = plan.tau;
+
+  // all that matters in one wave's hands
+  if (n >= 1 && n <= (uint32_t)kWave && plan.hi == INFINITY) {
+    const float z = __uint_as_float(entry.x);
+    const double w = exp(((double)z - (double)m) * invT);
+    FdShort k = fd_short(fkey(z), lane < (int)n ? fd_fixed(w, unit) : 0ull, (int)n, by_k, f.k, by_p,
+                         (double)f.p, (double)f.p * plan.Z * unit);
+    if (k.reached || by_k || plan.lo == plan.tau) {
+      if (wave != 0) return;
+      k.kept = k.kept && z >= tau;
+      double S;
+      const int y = fd_short_draw(k.kept, (int)entry.y, w, (int)n, a.tokens != nullptr, u, S);
+      const uint32_t low = ~wave_max_u32(k.kept ? ~fkey(z) : 0u);
+      if (lane == 0) {
+        a.plans[r].tau = unkey(low);
+        a.plans[r].invS = 1.0 / S;
+        if (a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
+      }
+      return;
+    }
+  }
+
+  const float4* gmax = a.gmax + (size_t)r * a.nseg;
+  const double* ssum = a.ssum + (size_t)r * a.nseg;
+  const uint2* part = a.part + (size_t)r * a.nseg;
   if (t < SPECV_EXP64_N) s.tbl[t] = kExp64Table[t];
   const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
-  const double invT = plan.invT;
-  const float m = plan.m;
-  const double unit = ldexp(1.0, 62 - (32 - __clz((a.V - 1) | 1)));
-  auto fixed = [&](float z) {
-    return (unsigned long long)__double2ll_rn(fd_weight(z, m, invT, s.tbl) * unit);
-  };
-
-  // the collected logits, one list, in order
-  uint32_t n = 0;
-  bool whole = true;
+  const FdExp weight(m, invT, s.tbl);
+  auto fixed = [&](float z) { return fd_fixed(weight(z), unit); };
+  bool whole = n <= (uint32_t)a.cap;
+  if (whole)
+    for (uint32_t e = t; e < n; e += kFdThreads) list[e] = __uint_as_float(found[e].x);
   double high = 0.0;
-  for (int g0 = 0; g0 < a.nseg; g0 += kFdThreads) {
-    const int g = g0 + t;
-    const uint32_t c = g < a.nseg ? slot_n[g] : 0u;
-    if (g < a.nseg) {
-      seg[g] = ssum[g];
-      high += seg[g];
-    }
-    whole = !__syncthreads_or(c > (uint32_t)kFdSlot) && whole;
-    unsigned long long total;
-    const uint32_t at = n + (uint32_t)fd_block_scan<kFdWaves>(s, c, total);
-    if (g < a.nseg) starts[g] = at;
-    n += (uint32_t)total;
+  for (int g = t; g < a.nseg; g += kFdThreads) {
+    seg[g] = ssum[g];
+    high += seg[g];
   }
-  whole = whole && n <= (uint32_t)a.list_cap;
-  high = fd_block_sum<kFdWaves>(s, high);
-  float tau = plan.tau;
-  if (whole) {
-    for (uint32_t e = t; e < n; e += kFdThreads) {
-      int g = 0;                                     // the last segment that starts at or before e
-      for (int step = 1 << 12; step; step >>= 1)
-        if (g + step < a.nseg && starts[g + step] <= e) g += step;
-      list[e] = a.slots[((size_t)r * a.nseg + g) * kFdSlot + (e - starts[g])];
-    }
-    __syncthreads();
-  }
-  if (plan.need & (kFdTopK | kFdTopP)) {
-    FdSource<T> src = {row, starts, 0u, list, n, true};
+  high = fd_block_sum<kFdWaves>(s, high);            // (its barriers serve the list too)
+  if (by_k || by_p) {
+    FdSource<T> src = {row, picks, 0u, list, n, true};
     auto each = [&](auto put) { src.each([&](float z) { put(fd_key<T>(z), z); }); };
     const uint32_t top = fd_key<T>(m);
     auto search = [&](float from, unsigned long long above) -> FdFound {
       FdFound k = {from > -INFINITY ? fd_key<T>(from) : kFdLowest<T>, true};
-      if (plan.need & kFdTopK)
+      if (by_k)
         k = fd_search<kFdThreads, false, false>(s, k.low, top, 0, (double)f.k, each,
                                                 [](float) { return 0ull; });
-      if (plan.need & kFdTopP) {
+      if (by_p) {
         double target = (double)f.p * plan.Z * unit;
-        if (plan.need & kFdTopK) {
+        if (by_k) {
           unsigned long long sum = 0, all;
           each([&](uint32_t key, float z) {
             if (key >= k.low) sum += fixed(z);
@@ -807,33 +943,27 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
           target = (double)f.p * (double)all;
         }
         k = fd_search<kFdThreads, true, false>(s, k.low, top, above, target, each, fixed);
-        k.reached = k.reached || (plan.need & kFdTopK);
       }
+      k.reached = k.reached || by_k;
       return k;
     };
     FdFound k = {0u, false};
-    const double target = (double)f.p * plan.Z;
-    const bool only_p = !(plan.need & kFdTopK);
-    if (whole && !(only_p && high >= target)) {
+    if (whole && (by_k || high < (double)f.p * plan.Z)) {
       k = search(plan.lo, (unsigned long long)__double2ll_rn(high * unit));
       // not reached: the threshold lies below the bracket, and below min-p's if
       // the bracket starts there
-      if (!k.reached) {
-        k.reached = plan.lo == plan.tau || !only_p;
-        k.low = plan.lo > -INFINITY ? fd_key<T>(plan.lo) : kFdLowest<T>;
-      }
+      if (!k.reached && plan.lo == plan.tau)
+        k = {plan.lo > -INFINITY ? fd_key<T>(plan.lo) : kFdLowest<T>, true};
     }
     if (!k.reached) {
       // the sample misled, or a list is too short for it: all of the row that matters
-      const float from = only_p ? fmaxf(plan.bound, plan.tau) : plan.lo;
+      const float from = by_k ? plan.lo : fmaxf(plan.bound, plan.tau);
       __syncthreads();
-      src.npick = fd_pick(s, starts, gmax, a.nseg, from);
+      src.npick = fd_pick(s, picks, gmax, a.nseg, from);
       src.listed = whole = false;
       k = search(from, 0ull);
     }
     tau = fmaxf(tau, fd_unkey<T>(k.low));
-  } else if (!whole) {
-    whole = true;                                    // min-p alone collects nothing
   }
 
   // the kept mass of each segment
@@ -841,19 +971,19 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
   if (whole) {
     if (n)
       for (int g = wave; g < a.nseg; g += kFdWaves) {
-        const uint32_t from = starts[g], to = g + 1 < a.nseg ? starts[g + 1] : n;
-        if (from == to) continue;
+        const uint2 p = part[g];
+        if (p.y == 0u) continue;
         double w = 0.0;
-        for (uint32_t e = from + lane; e < to; e += kWave)
-          if (list[e] >= tau) w += fd_weight(list[e], m, invT, s.tbl);
+        for (uint32_t e = lane; e < p.y; e += kWave)
+          if (list[p.x + e] >= tau) w += weight(list[p.x + e]);
         w = wave_sum(w);
         if (lane == 0) seg[g] += w;
       }
   } else {
     for (int g = t; g < a.nseg; g += kFdThreads) seg[g] = 0.0;
-    const uint32_t np = fd_pick(s, starts, gmax, a.nseg, tau);
+    const uint32_t np = fd_pick(s, picks, gmax, a.nseg, tau);
     for (uint32_t e = wave; e < np; e += kFdWaves) {
-      const uint32_t pick = starts[e];
+      const uint32_t pick = picks[e];
       float v[kFdGroups][N];
       fd_load(row, pick, lane, v);
       double w = 0.0;
@@ -861,20 +991,18 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
       for (int j = 0; j < kFdGroups; ++j)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (v[j][i] >= tau && v[j][i] > -INFINITY) w += fd_weight(v[j][i], m, invT, s.tbl);
+          if (v[j][i] >= tau && v[j][i] > -INFINITY) w += weight(v[j][i]);
       w = wave_sum(w);
       if (lane == 0) seg[pick >> 4] = w;
     }
   }
   __syncthreads();
-  if (wave == 0) {
-    double S;
-    const int y = fd_draw(row, seg, a.nseg, a.tokens != nullptr, u, tau, m, invT, s.tbl, S);
-    if (lane == 0) {
-      a.plans[r].tau = tau;
-      a.plans[r].invS = 1.0 / S;
-      if (a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
-    }
+  double S;
+  const int y = fd_draw(s, row, seg, a.nseg, a.tokens != nullptr, u, tau, weight, S);
+  if (t == 0) {
+    a.plans[r].tau = tau;
+    a.plans[r].invS = 1.0 / S;
+    if (a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
   }
 }
 
@@ -965,6 +1093,9 @@ constexpr int kFdOneV = 32768;
 struct FdOneShared {
   FdShared s;
   double group[kFdOneGroups];                       // their kept masses
+  uint2 few[kWave];                                 // a short list: logits and ids
+  double S;
+  float tau;
 };
 static_assert(((kFdOneV + 6) / 4 + 63) / 64 <= kFdOneGroups, "every group has its mass");
 
@@ -1015,10 +1146,9 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
   } else if (ok) {
     invT = 1.0 / (double)f.T;
     const bool by_k = f.k > 0 && f.k < a.V, by_p = f.p < 1.f;
-    const double unit = ldexp(1.0, 62 - (32 - __clz((a.V - 1) | 1)));
-    auto fixed = [&](float z) {
-      return (unsigned long long)__double2ll_rn(fd_weight(z, m, invT, s.tbl) * unit);
-    };
+    const double unit = fd_unit(a.V);
+    const FdExp weight(m, invT, s.tbl);
+    auto fixed = [&](float z) { return fd_fixed(weight(z), unit); };
     auto each = [&](auto put) {
       for (int q = t; q < nv; q += kFdThreads) {
         float v[N];
@@ -1029,20 +1159,60 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
     };
     const uint32_t high = fd_key<T>(m);
     tau = -INFINITY;
-    if (f.mp > 0.f) tau = fd_min_p_threshold(m, invT, f.mp, s.tbl);
+    if (f.mp > 0.f) tau = fd_min_p_threshold(m, f.T, weight, f.mp);
+    // logits put on a list of 64 (in LDS, any order), how many in s.npick
+    if (t == 0) s.npick = 0;
+    auto put = [&](float z, int id) {
+      const uint32_t at = atomicAdd(&s.npick, 1u);
+      if (at < (uint32_t)kWave) o.few[at] = make_uint2(__float_as_uint(z), (uint32_t)id);
+    };
+    bool done = false;
     uint32_t low = kFdLowest<T>;
     if (by_k) {
       if (f.k <= kFdThreads) {
         // at least k tokens reach the k-th largest of the threads' maxima
         const FdFound k = fd_search<kFdThreads, false, true>(
-            s, low, high, 0, (double)f.k, [&](auto put) { put(fd_key<T>(big), big); },
+            s, low, high, 0, (double)f.k, [&](auto add) { add(fd_key<T>(big), big); },
             [](float) { return 0ull; });
         if (k.reached) low = k.low;
+        if (fd_key<T>(big) >= low)
+          for (int q = t; q < nv; q += kFdThreads) {
+            float v[N];
+            unpack(kept[q], v, T{});
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+              if (fd_key<T>(v[j]) >= low) put(v[j], row.first(q) + j);
+          }
+        __syncthreads();
+        const int n = (int)s.npick;
+        if (n <= kWave) {
+          // all that matters in one wave's hands
+          done = true;
+          if (wave == 0) {
+            const uint2 e = o.few[lane];
+            const float z = lane < n ? __uint_as_float(e.x) : m;
+            const double w = weight(z);
+            const FdShort k1 = fd_short(fkey(z), lane < n ? fd_fixed(w, unit) : 0ull, n, true, f.k, by_p,
+                                        (double)f.p, 0.0);
+            const bool in = k1.kept && z >= tau;
+            double S;
+            y = fd_short_draw(in, (int)e.y, w, n, a.tokens != nullptr, u, S);
+            const uint32_t least = ~wave_max_u32(in ? ~fkey(z) : 0u);
+            if (lane == 0) {
+              o.tau = unkey(least);
+              o.S = S;
+            }
+          }
+          __syncthreads();
+          tau = o.tau;
+          invS = 1.0 / o.S;
+        }
       }
-      low = fd_search<kFdThreads, false, false>(s, low, high, 0, (double)f.k, each,
-                                                [](float) { return 0ull; }).low;
+      if (!done)
+        low = fd_search<kFdThreads, false, false>(s, low, high, 0, (double)f.k, each,
+                                                  [](float) { return 0ull; }).low;
     }
-    if (by_p && by_k) {
+    if (by_p && by_k && !done) {
       unsigned long long sum = 0, all;
       each([&](uint32_t key, float z) {
         if (key >= low) sum += fixed(z);
@@ -1050,49 +1220,77 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
       fd_block_scan<kFdWaves>(s, sum, all);
       low = fd_search<kFdThreads, true, false>(s, low, high, 0, (double)f.p * (double)all, each,
                                                fixed).low;
-    } else if (by_p) {
-      const double width = 1e-6 - log((1.0 - (double)f.p) / a.V), per = kFdBins / width;
-      auto bin = [&](float z) { return ((double)m - (double)z) * invT * per; };
+    } else if (by_p && !by_k) {
+      const double width = 1e-6 - log((1.0 - (double)f.p) / a.V);
+      const double per = kFdBins / width, bins = per / SPECV_EXP64_INV_L;
       for (int i = t; i < kFdBins; i += kFdThreads) s.mass[i] = 0;
       __syncthreads();
-      unsigned long long tail = 0, all, ignore;
+      unsigned long long tail = 0, all, rest;
       each([&](uint32_t, float z) {
-        if (z > -INFINITY) {
-          const unsigned long long w = fixed(z);
-          const double x = bin(z);
-          if (x < kFdBins) atomicAdd(&s.mass[(int)x], w);
-          else tail += w;
-        }
+        const double x = weight.units(z), bin = -x * bins;
+        const unsigned long long w = fd_fixed(weight.of_units(x), unit);
+        if (bin < kFdBins) atomicAdd(&s.mass[(int)bin], w);
+        else tail += w;
       });
-      __syncthreads();
+      fd_block_scan<kFdWaves>(s, tail, rest);        // (its barriers serve the bins too)
       const unsigned long long x0 = s.mass[2 * t], x1 = s.mass[2 * t + 1];
-      unsigned long long before = fd_block_scan<kFdWaves>(s, x0 + x1, all);
-      fd_block_scan<kFdWaves>(s, tail, ignore);
-      const double target = (double)f.p * (double)(all + ignore);
+      const unsigned long long before = fd_block_scan<kFdWaves>(s, x0 + x1, all);
+      const double target = (double)f.p * (double)(all + rest);
       // the last bin that holds something and has less than the target before it
       uint32_t mine = 0;
       if (x0 && (double)before < target) mine = 2u * t + 1u;
       if (x1 && (double)(before + x0) < target) mine = 2u * t + 2u;
       const uint32_t found = fd_block_max<kFdWaves>(s, mine);
       if (mine == found && found) s.above = found & 1u ? before : before + x0;
-      __syncthreads();
+      // its logits
       const int at = (int)found - 1;
-      // its values, with room for the edges' rounding; membership is by the bin
+      auto in_bin = [&](float z) {
+        const double bin = -weight.units(z) * bins;
+        return bin >= at && bin < at + 1;
+      };
+      // (a cheap look first: their range, with room for the edges' rounding)
       const double z1 = (double)m - (double)f.T * (at / per), z0 = (double)m - (double)f.T * ((at + 1) / per);
       const double room = 1e-12 * (fabs((double)m) + fabs(z0) + fabs(z1));
-      const uint32_t k0 = fd_key<T>((float)(z0 - room)), k1 = fd_key<T>((float)(z1 + room));
-      low = fd_search<kFdThreads, true, false>(
-                s, max(kFdLowest<T>, k0 - min(k0, 1u)), min(high, k1 + 1u), s.above, target,
-                [&](auto put) {
-                  each([&](uint32_t key, float z) {
-                    const double x = bin(z);
-                    if (x >= at && x < at + 1) put(key, z);
-                  });
-                },
-                fixed).low;
+      const uint32_t e0 = fd_key<T>((float)(z0 - room)), e1 = fd_key<T>((float)(z1 + room));
+      const uint32_t k0 = max(kFdLowest<T>, e0 - min(e0, 1u)), k1 = min(high, e1 + 1u);
+      for (int q = t; q < nv; q += kFdThreads) {
+        float v[N];
+        unpack(kept[q], v, T{});
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const uint32_t key = fd_key<T>(v[j]);
+          if (key >= k0 && key <= k1 && in_bin(v[j])) put(v[j], 0);
+        }
+      }
+      __syncthreads();
+      const int n = (int)s.npick;
+      const unsigned long long above = s.above;
+      if (n <= kWave) {                              // every wave for itself
+        const float z = lane < n ? __uint_as_float(o.few[lane].x) : m;
+        const unsigned long long w = lane < n ? fixed(z) : 0ull;
+        const int lo32 = (int)(uint32_t)w, hi32 = (int)(uint32_t)(w >> 32);
+        const uint32_t key = fd_key<T>(z);
+        unsigned long long over = above;
+        for (int j = 0; j < n; ++j) {
+          const unsigned long long x =
+              (unsigned long long)(uint32_t)lane_value(hi32, j) << 32 | (uint32_t)lane_value(lo32, j);
+          over += (uint32_t)lane_value((int)key, j) > key ? x : 0ull;
+        }
+        low = ~wave_max_u32(lane < n && (double)over < target ? ~key : 0u);
+      } else {
+        low = fd_search<kFdThreads, true, false>(
+                  s, k0, k1, above, target,
+                  [&](auto add) {
+                    each([&](uint32_t key, float z) {
+                      if (key >= k0 && key <= k1 && in_bin(z)) add(key, z);
+                    });
+                  },
+                  fixed).low;
+      }
     }
-    if (by_k || by_p) tau = fmaxf(tau, fd_unkey<T>(low));
+    if ((by_k || by_p) && !done) tau = fmaxf(tau, fd_unkey<T>(low));
 
+    if (!done) {
     // kept mass of each group of 64 vectors
     const int ngroup = (nv + kWave - 1) / kWave;
     for (int g = wave; g < ngroup; g += kFdWaves) {
@@ -1106,7 +1304,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
       if (__any(some)) {
 #pragma unroll
         for (int j = 0; j < N; ++j)
-          if (v[j] >= tau && v[j] > -INFINITY) w += fd_weight(v[j], m, invT, s.tbl);
+          if (v[j] >= tau && v[j] > -INFINITY) w += weight(v[j]);
         w = wave_sum(w);
       }
       if (lane == 0) o.group[g] = w;
@@ -1149,7 +1347,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
         double x[N], sum = 0.0;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          x[j] = v[j] >= tau && v[j] > -INFINITY ? fd_weight(v[j], m, invT, s.tbl) : 0.0;
+          x[j] = v[j] >= tau && v[j] > -INFINITY ? weight(v[j]) : 0.0;
           sum += x[j];
         }
         double here = base + wave_shr1(wave_incl_scan(sum));
@@ -1166,6 +1364,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
         y = hit ? lane_value(first, __ffsll((unsigned long long)hit) - 1)
                 : lane_value(tail, 63 - __clzll((long long)any));
       }
+    }
     }
   }
   if (t == 0 && a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
@@ -1203,35 +1402,42 @@ bool filter_fits(int B, int L, int V, bool bf16) {
 
 // Parts of the workspace, 16-byte aligned.
 struct FdLayout {
-  size_t gmax, ssum, slot_n, slots, bytes;
+  size_t gmax, ssum, part, list, bytes;
+  int cap;
 };
-FdLayout fd_layout(size_t rows, int nseg) {
-  const size_t segs = (rows * nseg + 3) / 4 * 4;
+FdLayout fd_layout(size_t rows, int V, int nseg) {
+  const size_t segs = (rows * nseg + 1) / 2 * 2;
   FdLayout w;
+  w.cap = min(V, kFdListCap);
   w.gmax = rows * sizeof(FdPlan);
   w.ssum = w.gmax + segs * sizeof(float4);
-  w.slot_n = w.ssum + segs * sizeof(double);
-  w.slots = w.slot_n + segs * sizeof(uint32_t);
-  w.bytes = w.slots + segs * kFdSlot * sizeof(float);
+  w.part = w.ssum + segs * sizeof(double);
+  w.list = w.part + segs * sizeof(uint2);
+  w.bytes = w.list + rows * w.cap * sizeof(uint2);
   return w;
 }
 
 size_t filter_workspace_bytes(int B, int L, int V, bool bf16) {
   if (V <= kFdOneV) return 0;
-  return fd_layout((size_t)B * L, fd_segs(V, bf16)).bytes;
+  return fd_layout((size_t)B * L, V, fd_segs(V, bf16)).bytes;
 }
 
-// LDS of the row kernel: the list takes what a CU has left, and no more than V.
-constexpr int kFdLds = 159 * 1024;                  // (the rest: the votes of __syncthreads_or)
+// The most LDS that a kernel asks for (the rest: the votes of __syncthreads_or).
+constexpr int kFdLds = 159 * 1024;
+
+template <typename F>
+hipError_t fd_allow_lds(F* kernel) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             hipFuncAttributeMaxDynamicSharedMemorySize, kFdLds);
+}
 
 template <typename T>
-hipError_t fd_run(FdArgs a, size_t rows, bool probs_bf16, hipStream_t stream) {
+hipError_t fd_run(const FdArgs& a, size_t rows, bool probs_bf16, hipStream_t stream) {
   if (a.V <= kFdOneV) {
     const auto one = probs_bf16 ? filter_one_kernel<T, bf16_t> : filter_one_kernel<T, float>;
     constexpr int N = Elem<T>::kPerVec;
     const int lds = ((int)sizeof(FdOneShared) + 15) / 16 * 16 + (a.V + 2 * (N - 1)) / N * 16;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(one),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kFdLds);
+    const hipError_t e = fd_allow_lds(one);
     if (e != hipSuccess) return e;
     one<<<dim3((unsigned)rows), dim3(kFdThreads), lds, stream>>>(a);
     return hipGetLastError();
@@ -1239,7 +1445,9 @@ hipError_t fd_run(FdArgs a, size_t rows, bool probs_bf16, hipStream_t stream) {
   const int nblk = fd_blocks(a.V, sizeof(T) == 2);
   const dim3 grid((unsigned)(rows * nblk));
   filter_stats_kernel<T><<<grid, dim3(kFdStatThreads), 0, stream>>>(a, nblk);
-  const int fixed = (int)sizeof(FdShared) + a.nseg * (int)(sizeof(double) + sizeof(uint32_t));
+  const int fixed = (int)sizeof(FdShared) + a.nseg * (int)sizeof(double);
+  hipError_t e = fd_allow_lds(filter_plan_kernel<T>);
+  if (e != hipSuccess) return e;
   filter_plan_kernel<T><<<dim3((unsigned)rows), dim3(kFdPlanThreads), fixed, stream>>>(a);
   // one setting for all rows that leaves nothing to collect ends here
   const specv_filters_t& f = a.f;
@@ -1248,12 +1456,10 @@ hipError_t fd_run(FdArgs a, size_t rows, bool probs_bf16, hipStream_t stream) {
   const bool greedy = !f.temperature_array && f.temperature == 0.f;
   if (!plain && !greedy) {
     filter_collect_kernel<T><<<grid, dim3(kFdStatThreads), 0, stream>>>(a, nblk);
-    a.list_cap = min(a.V, (kFdLds - fixed) / (int)sizeof(float));
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(filter_row_kernel<T>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kFdLds);
+    e = fd_allow_lds(filter_row_kernel<T>);
     if (e != hipSuccess) return e;
-    filter_row_kernel<T><<<dim3((unsigned)rows), dim3(kFdThreads),
-                           fixed + a.list_cap * (int)sizeof(float), stream>>>(a);
+    const int lds = fixed + a.nseg * (int)sizeof(uint32_t) + a.cap * (int)sizeof(float);
+    filter_row_kernel<T><<<dim3((unsigned)rows), dim3(kFdThreads), lds, stream>>>(a);
   }
   if (a.probs) {
     if (probs_bf16) filter_probs_kernel<T, bf16_t><<<grid, dim3(kFdStatThreads), 0, stream>>>(a, nblk);
@@ -1270,13 +1476,14 @@ hipError_t launch_filter(const void* logits, long long zsb, long long zsl, bool 
   FdArgs a = {logits, zsb, zsl, L, V, f, u, usb, usl, tokens, tsb, tsl, probs, psb, psl};
   const size_t rows = (size_t)B * L;
   a.nseg = fd_segs(V, bf16);
-  const FdLayout w = fd_layout(rows, a.nseg);
+  const FdLayout w = fd_layout(rows, V, a.nseg);
   char* base = static_cast<char*>(workspace);
   a.plans = reinterpret_cast<FdPlan*>(base);
   a.gmax = reinterpret_cast<float4*>(base + w.gmax);
   a.ssum = reinterpret_cast<double*>(base + w.ssum);
-  a.slot_n = reinterpret_cast<uint32_t*>(base + w.slot_n);
-  a.slots = reinterpret_cast<float*>(base + w.slots);
+  a.part = reinterpret_cast<uint2*>(base + w.part);
+  a.list = reinterpret_cast<uint2*>(base + w.list);
+  a.cap = w.cap;
   return bf16 ? fd_run<bf16_t>(a, rows, probs_bf16, stream)
               : fd_run<float>(a, rows, probs_bf16, stream);
 }
