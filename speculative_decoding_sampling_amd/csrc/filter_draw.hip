@@ -170,6 +170,17 @@ struct FdExp {
     return ldexp(fma(tj, q * f, tj), k >> SPECV_EXP64_LOG2N);
   }
   __device__ __forceinline__ double operator()(float z) const { return of_units(units(z)); }
+  // The sum of those at or above tau, finite.  No branches: the weights' chains
+  // of dependent operations and table reads overlap.
+  template <int N>
+  __device__ __forceinline__ double sum(const float (&v)[N], float tau) const {
+    double w[N], s = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = (*this)(v[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) s += v[i] >= tau && v[i] > -INFINITY ? w[i] : 0.0;
+    return s;
+  }
 };
 
 // Weights as whole multiples of 2^-s: the sum with 2^52 leaves them in its low
@@ -615,6 +626,27 @@ __device__ __forceinline__ int fd_draw(FdShared& s, const FdRow<T>& row, const d
   return y < 0 ? end : y;
 }
 
+// Masses put into bins of their distance from the maximum (bins to a unit of
+// FdExp), past the last into tail.
+template <int N>
+__device__ __forceinline__ void fd_spread(FdShared& s, const FdExp& weight, const float (&v)[N],
+                                          double unit, double bins, int nbin,
+                                          unsigned long long& tail) {
+  unsigned long long w[N];
+  double b[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const double x = weight.units(v[i]);
+    w[i] = fd_fixed(weight.of_units(x), unit);
+    b[i] = -x * bins;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (b[i] < nbin) atomicAdd(&s.mass[(int)b[i]], w[i]);
+    else tail += w[i];
+  }
+}
+
 // The bracket of a top-p threshold from a sample of the row.  With M(x) the mass
 // of the tokens x or more below the maximum (in units of T), the threshold lies
 // where M falls below B = (1 - p) Z.  The sample gives M as scale sum w; tokens
@@ -643,16 +675,7 @@ __device__ __forceinline__ void fd_sample(FdShared& s, const FdRow<T>& row, cons
     row.load(c < n ? q : row.vecs(), v[i]);          // past the row: -inf
   }
 #pragma unroll
-  for (int i = 0; i < kSweeps; ++i)
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (v[i][j] > -INFINITY) {
-        const double x = weight.units(v[i][j]);
-        const unsigned long long w = fd_fixed(weight.of_units(x), unit);
-        const double b = -x * bins;
-        if (b < kFdSampleBins) atomicAdd(&s.mass[(int)b], w);
-        else tail += w;
-      }
+  for (int i = 0; i < kSweeps; ++i) fd_spread(s, weight, v[i], unit, bins, kFdSampleBins, tail);
   unsigned long long all;
   fd_block_scan<kWaves>(s, tail, all);
   // thread t owns bins top - 2 t and the one below: sums from the far end
@@ -824,11 +847,10 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_collect_kernel(FdArgs a
   if (bits) {
     if (sums) {
       const FdExp weight(m, invT, tbl);
+      const uint32_t over = fd_reach(gm, hi);
 #pragma unroll
       for (int j = 0; j < kFdGroups; ++j)
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (v[j][i] >= hi) w += weight(v[j][i]);
+        if (over >> j & 1u) w += weight.sum(v[j], hi);
       w = wave_sum(w);
     }
 #pragma unroll
@@ -915,12 +937,14 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
   const FdExp weight(m, invT, s.tbl);
   auto fixed = [&](float z) { return fd_fixed(weight(z), unit); };
   bool whole = n <= (uint32_t)a.cap;
-  if (whole)
-    for (uint32_t e = t; e < n; e += kFdThreads) list[e] = __uint_as_float(found[e].x);
   double high = 0.0;
   for (int g = t; g < a.nseg; g += kFdThreads) {
     seg[g] = ssum[g];
     high += seg[g];
+  }
+  if (whole) {
+#pragma unroll 4
+    for (uint32_t e = t; e < n; e += kFdThreads) list[e] = __uint_as_float(found[e].x);
   }
   high = fd_block_sum<kFdWaves>(s, high);            // (its barriers serve the list too)
   if (by_k || by_p) {
@@ -969,15 +993,21 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
   // the kept mass of each segment
   __syncthreads();
   if (whole) {
+    // 16 lanes a segment
     if (n)
-      for (int g = wave; g < a.nseg; g += kFdWaves) {
+      for (int g = t / 16; g < a.nseg; g += kFdThreads / 16) {
         const uint2 p = part[g];
-        if (p.y == 0u) continue;
         double w = 0.0;
-        for (uint32_t e = lane; e < p.y; e += kWave)
-          if (list[p.x + e] >= tau) w += weight(list[p.x + e]);
-        w = wave_sum(w);
-        if (lane == 0) seg[g] += w;
+        for (uint32_t e = t % 16; e < p.y; e += 16) {
+          const float z = list[p.x + e];
+          const double x = weight(z);
+          w += z >= tau ? x : 0.0;
+        }
+        w += dpp_f64<0xb1>(w);
+        w += dpp_f64<0x4e>(w);
+        w += dpp_f64<0x141>(w);
+        w += dpp_f64<0x140>(w);
+        if (t % 16 == 0) seg[g] += w;
       }
   } else {
     for (int g = t; g < a.nseg; g += kFdThreads) seg[g] = 0.0;
@@ -988,10 +1018,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
       fd_load(row, pick, lane, v);
       double w = 0.0;
 #pragma unroll
-      for (int j = 0; j < kFdGroups; ++j)
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (v[j][i] >= tau && v[j][i] > -INFINITY) w += weight(v[j][i]);
+      for (int j = 0; j < kFdGroups; ++j) w += weight.sum(v[j], tau);
       w = wave_sum(w);
       if (lane == 0) seg[pick >> 4] = w;
     }
@@ -1226,12 +1253,11 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
       for (int i = t; i < kFdBins; i += kFdThreads) s.mass[i] = 0;
       __syncthreads();
       unsigned long long tail = 0, all, rest;
-      each([&](uint32_t, float z) {
-        const double x = weight.units(z), bin = -x * bins;
-        const unsigned long long w = fd_fixed(weight.of_units(x), unit);
-        if (bin < kFdBins) atomicAdd(&s.mass[(int)bin], w);
-        else tail += w;
-      });
+      for (int q = t; q < nv; q += kFdThreads) {
+        float v[N];
+        unpack(kept[q], v, T{});
+        fd_spread(s, weight, v, unit, bins, kFdBins, tail);
+      }
       fd_block_scan<kFdWaves>(s, tail, rest);        // (its barriers serve the bins too)
       const unsigned long long x0 = s.mass[2 * t], x1 = s.mass[2 * t + 1];
       const unsigned long long before = fd_block_scan<kFdWaves>(s, x0 + x1, all);
@@ -1301,12 +1327,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
       bool some = false;
 #pragma unroll
       for (int j = 0; j < N; ++j) some = some || (v[j] >= tau && v[j] > -INFINITY);
-      if (__any(some)) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (v[j] >= tau && v[j] > -INFINITY) w += weight(v[j]);
-        w = wave_sum(w);
-      }
+      if (__any(some)) w = wave_sum(weight.sum(v, tau));
       if (lane == 0) o.group[g] = w;
     }
     __syncthreads();
