@@ -48,6 +48,7 @@ constexpr int kFdGroups = 4;                        // groups of a segment
 constexpr int kFdSegVecs = kFdGroups * kWave;       // 4 KB of logits
 constexpr int kFdStatThreads = 256;
 constexpr int kFdPlanThreads = 512;
+constexpr int kFdCollectBlocks = 8 * 256;           // eight to a CU
 constexpr int kFdListCap = 16384;                   // collected logits of a row
 constexpr int kFdSampleBins = 2 * kFdPlanThreads;
 
@@ -88,6 +89,8 @@ struct FdArgs {
   uint2* part;                      // [B L][nseg] where a segment's logits of the bracket stand in
                                     // the row's list, and how many they are
   uint2* list;                      // [B L][cap] those logits, with their ids
+  int* nitem;                       // what there is to collect: how many segments,
+  uint2* items;                     // and which (row; segment and groups as fd_pick has them)
   int nseg, cap;
 };
 
@@ -217,6 +220,7 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_stats_kernel(FdArgs a, 
     exp64_stage_table<kFdStatThreads>(tbl);
     __syncthreads();
   }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.nitem = 0;     // for the plans, which follow
   if (g >= a.nseg) return;
   float top[kFdGroups], m = -INFINITY;
 #pragma unroll
@@ -705,6 +709,7 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   FdShared& s = *reinterpret_cast<FdShared*>(dyn);
   double* seg = reinterpret_cast<double*>(dyn + sizeof(FdShared));
+  uint32_t* picks = reinterpret_cast<uint32_t*>(seg + a.nseg);
   constexpr int N = FdRow<T>::N, kWaves = kFdPlanThreads / kWave;
   const int r = blockIdx.x, b = r / a.L, l = r % a.L, t = threadIdx.x;
   const int lane = t % kWave, wave = t / kWave;
@@ -810,49 +815,59 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
   if (t == 0) {
     a.plans[r] = plan;
     if (a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
+    s.npick = 0;
   }
+  if (plan.need == kFdDone) return;
+  // the segments that reach the bracket; the others have nothing
+  __syncthreads();
+  for (int g = t; g < a.nseg; g += kFdPlanThreads) {
+    const float4 x = gmax[g];
+    const bool some = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) > -INFINITY;
+    const uint32_t bits = some ? fd_reach(x, plan.lo) : 0u;
+    if (bits) {
+      picks[atomicAdd(&s.npick, 1u)] = (uint32_t)g << 4 | bits;
+    } else {
+      a.ssum[(size_t)r * a.nseg + g] = 0.0;
+      a.part[(size_t)r * a.nseg + g] = make_uint2(0u, 0u);
+    }
+  }
+  __syncthreads();
+  if (t == 0) s.above = (unsigned long long)atomicAdd(a.nitem, (int)s.npick);
+  __syncthreads();
+  for (uint32_t i = t; i < s.npick; i += kFdPlanThreads) a.items[s.above + i] = make_uint2((uint32_t)r, picks[i]);
 }
 
-// One wave a segment that reaches the row's bracket.
+// One wave a segment that reaches its row's bracket: as many waves as the chip
+// holds take them in turn.
 template <typename T>
-__global__ __launch_bounds__(kFdStatThreads) void filter_collect_kernel(FdArgs a, int nblk) {
-  constexpr int N = FdRow<T>::N;
+__global__ __launch_bounds__(kFdStatThreads) void filter_collect_kernel(FdArgs a) {
+  constexpr int N = FdRow<T>::N, kWaves = kFdStatThreads / kWave;
   __shared__ double tbl[SPECV_EXP64_N];
-  const int r = blockIdx.x / nblk, b = r / a.L, l = r % a.L;
   const int lane = threadIdx.x % kWave;
-  const int g = (blockIdx.x % nblk) * (kFdStatThreads / kWave) +
-                __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const size_t at = (size_t)r * a.nseg + g;
-  FdPlan* plan = a.plans + r;
-  Exp64Stage<kFdStatThreads> stage;
-  stage.fetch();
-  const float4 gm = g < a.nseg ? a.gmax[at] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-  const float lo = plan->lo, hi = plan->hi, m = plan->m;
-  const double invT = plan->invT;
-  if (plan->need == kFdDone) return;                 // uniform over the block
-  const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
-  const uint32_t bits = gm.x > -INFINITY || gm.y > -INFINITY || gm.z > -INFINITY || gm.w > -INFINITY
-                            ? fd_reach(gm, lo) : 0u;
-  // weights from hi up
-  const bool sums = gm.x >= hi || gm.y >= hi || gm.z >= hi || gm.w >= hi;
-  float v[kFdGroups][N];
-  if (bits) fd_load(row, (uint32_t)g << 4 | bits, lane, v);
-  if (__syncthreads_or(sums)) {
-    stage.store(tbl);
-    __syncthreads();
-  }
-  if (g >= a.nseg) return;
-  double w = 0.0;
-  uint32_t n = 0, from = 0;
-  if (bits) {
-    if (sums) {
-      const FdExp weight(m, invT, tbl);
-      const uint32_t over = fd_reach(gm, hi);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int items = *a.nitem;
+  if ((int)blockIdx.x * kWaves >= items) return;
+  exp64_stage_table<kFdStatThreads>(tbl);
+  __syncthreads();
+  for (int i = blockIdx.x * kWaves + wave; i < items; i += gridDim.x * kWaves) {
+    const uint2 item = a.items[i];
+    const int r = (int)item.x, b = r / a.L, l = r % a.L, g = (int)(item.y >> 4);
+    const size_t at = (size_t)r * a.nseg + g;
+    FdPlan* plan = a.plans + r;
+    const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
+    float v[kFdGroups][N];
+    fd_load(row, item.y, lane, v);
+    const float lo = plan->lo, hi = plan->hi;
+    const uint32_t over = fd_reach(a.gmax[at], hi);
+    double w = 0.0;
+    if (over) {
+      const FdExp weight(plan->m, plan->invT, tbl);
 #pragma unroll
       for (int j = 0; j < kFdGroups; ++j)
         if (over >> j & 1u) w += weight.sum(v[j], hi);
       w = wave_sum(w);
     }
+    uint32_t n = 0, from = 0;
 #pragma unroll
     for (int j = 0; j < kFdGroups; ++j)
 #pragma unroll
@@ -877,10 +892,10 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_collect_kernel(FdArgs a
             ++mine;
           }
     }
-  }
-  if (lane == 0) {
-    a.ssum[at] = w;
-    a.part[at] = make_uint2(from, n);
+    if (lane == 0) {
+      a.ssum[at] = w;
+      a.part[at] = make_uint2(from, n);
+    }
   }
 }
 
@@ -1423,7 +1438,7 @@ bool filter_fits(int B, int L, int V, bool bf16) {
 
 // Parts of the workspace, 16-byte aligned.
 struct FdLayout {
-  size_t gmax, ssum, part, list, bytes;
+  size_t gmax, ssum, part, list, items, nitem, bytes;
   int cap;
 };
 FdLayout fd_layout(size_t rows, int V, int nseg) {
@@ -1434,7 +1449,9 @@ FdLayout fd_layout(size_t rows, int V, int nseg) {
   w.ssum = w.gmax + segs * sizeof(float4);
   w.part = w.ssum + segs * sizeof(double);
   w.list = w.part + segs * sizeof(uint2);
-  w.bytes = w.list + rows * w.cap * sizeof(uint2);
+  w.items = w.list + rows * w.cap * sizeof(uint2);
+  w.nitem = w.items + segs * sizeof(uint2);
+  w.bytes = w.nitem + 16;
   return w;
 }
 
@@ -1469,17 +1486,19 @@ hipError_t fd_run(const FdArgs& a, size_t rows, bool probs_bf16, hipStream_t str
   const int fixed = (int)sizeof(FdShared) + a.nseg * (int)sizeof(double);
   hipError_t e = fd_allow_lds(filter_plan_kernel<T>);
   if (e != hipSuccess) return e;
-  filter_plan_kernel<T><<<dim3((unsigned)rows), dim3(kFdPlanThreads), fixed, stream>>>(a);
+  const int lds_plan = fixed + a.nseg * (int)sizeof(uint32_t);
+  filter_plan_kernel<T><<<dim3((unsigned)rows), dim3(kFdPlanThreads), lds_plan, stream>>>(a);
   // one setting for all rows that leaves nothing to collect ends here
   const specv_filters_t& f = a.f;
   const bool plain = !f.top_k_array && !f.top_p_array && !f.min_p_array &&
                      (f.top_k == 0 || f.top_k >= a.V) && f.top_p == 1.f && f.min_p == 0.f;
   const bool greedy = !f.temperature_array && f.temperature == 0.f;
   if (!plain && !greedy) {
-    filter_collect_kernel<T><<<grid, dim3(kFdStatThreads), 0, stream>>>(a, nblk);
+    const size_t blocks = min(rows * nblk, (size_t)kFdCollectBlocks);
+    filter_collect_kernel<T><<<dim3((unsigned)blocks), dim3(kFdStatThreads), 0, stream>>>(a);
     e = fd_allow_lds(filter_row_kernel<T>);
     if (e != hipSuccess) return e;
-    const int lds = fixed + a.nseg * (int)sizeof(uint32_t) + a.cap * (int)sizeof(float);
+    const int lds = lds_plan + a.cap * (int)sizeof(float);
     filter_row_kernel<T><<<dim3((unsigned)rows), dim3(kFdThreads), lds, stream>>>(a);
   }
   if (a.probs) {
@@ -1504,6 +1523,8 @@ hipError_t launch_filter(const void* logits, long long zsb, long long zsl, bool 
   a.ssum = reinterpret_cast<double*>(base + w.ssum);
   a.part = reinterpret_cast<uint2*>(base + w.part);
   a.list = reinterpret_cast<uint2*>(base + w.list);
+  a.items = reinterpret_cast<uint2*>(base + w.items);
+  a.nitem = reinterpret_cast<int*>(base + w.nitem);
   a.cap = w.cap;
   return bf16 ? fd_run<bf16_t>(a, rows, probs_bf16, stream)
               : fd_run<float>(a, rows, probs_bf16, stream);
