@@ -152,27 +152,38 @@ __device__ __forceinline__ bool fd_wants_sums(const FdParams& f, int V) {
   return f.ok && f.T > 0.f && (f.k == 0 || f.k >= V) && (f.p < 1.f || f.mp == 0.f);
 }
 
-// Weights exp((z - m) / T), at most 1, by the table of exp64.h: with y = (z - m) N
-// / (T ln2), k = rint(y) and f = y - k in [-1/2, 1/2] the weight is 2^(k / N) 2^(f / N),
-// the second factor 1 + p(f).  Working in units of ln2 / N spares exp64's second
-// product; y's rounding costs |z - m| / T 2^-52 of the weight at most.
+// Weights exp((z - m) / T), at most 1: exp64.h's method and table, whose entries
+// stand in LDS with their index taken from the exponent's place, so that adding
+// k there leaves 2^(k / N) in one operation.  What would be below e^-700 stays
+// there and counts as nothing in a draw; -inf is told apart by whoever sums.
+constexpr double kFdNothing = 1e-290;
+__device__ __forceinline__ double fd_table_entry(int i) {
+  const double v = kExp64Table[i];
+  return __hiloint2double(__double2hiint(v) - (i << (20 - SPECV_EXP64_LOG2N)), __double2loint(v));
+}
+template <int NT>
+__device__ __forceinline__ void fd_stage_table(double* tbl) {
+  for (int i = threadIdx.x; i < SPECV_EXP64_N; i += NT) tbl[i] = fd_table_entry(i);
+}
 struct FdExp {
-  double m, c;                                       // c = N / (T ln2)
+  double m, invT;
   const double* tbl;
   __device__ __forceinline__ FdExp(double m, double invT, const double* tbl)
-      : m(m), c(invT * SPECV_EXP64_INV_L), tbl(tbl) {}
-  __device__ __forceinline__ double units(float z) const { return ((double)z - m) * c; }
-  __device__ __forceinline__ double of_units(double y) const {
-    y = fmax(y, -551000.0);                          // below e^-745: 0
-    const double t = y + SPECV_EXP64_SHIFT, f = y - (t - SPECV_EXP64_SHIFT);
-    const int k = (int)(unsigned)__double_as_longlong(t);
-    constexpr double L = SPECV_EXP64_L;
-    double q = fma(f, L * L * L / 6, L * L / 2);
-    q = fma(f, q, L);
-    const double tj = tbl[k & (SPECV_EXP64_N - 1)];
-    return ldexp(fma(tj, q * f, tj), k >> SPECV_EXP64_LOG2N);
+      : m(m), invT(invT), tbl(tbl) {}
+  // x = (z - m) / T, and its weight
+  __device__ __forceinline__ double arg(float z) const { return ((double)z - m) * invT; }
+  __device__ __forceinline__ double of(double x) const {
+    x = fmax(x, -700.0);
+    const double t = fma(x, SPECV_EXP64_INV_L, SPECV_EXP64_SHIFT);
+    const double r = fma(-(t - SPECV_EXP64_SHIFT), SPECV_EXP64_L, x);
+    double q = fma(r, SPECV_EXP64_C3, 0.5);
+    q = fma(r, q, 1.0);
+    const int k = __double2loint(t);
+    const double e = tbl[k & (SPECV_EXP64_N - 1)];
+    const double tj = __hiloint2double(__double2hiint(e) + (k << (20 - SPECV_EXP64_LOG2N)), __double2loint(e));
+    return fma(tj, r * q, tj);
   }
-  __device__ __forceinline__ double operator()(float z) const { return of_units(units(z)); }
+  __device__ __forceinline__ double operator()(float z) const { return of(arg(z)); }
   // The sum of those at or above tau, finite.  No branches: the weights' chains
   // of dependent operations and table reads overlap.
   template <int N>
@@ -217,7 +228,7 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_stats_kernel(FdArgs a, 
   const FdParams f = fd_params(a.f, b);
   const bool sums = fd_wants_sums(f, a.V);
   if (sums) {
-    exp64_stage_table<kFdStatThreads>(tbl);
+    fd_stage_table<kFdStatThreads>(tbl);
     __syncthreads();
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.nitem = 0;     // for the plans, which follow
@@ -544,7 +555,7 @@ __device__ __forceinline__ int fd_short_draw(bool kept, int id, double w, int n,
   const double incl = wave_incl_scan(w);
   S = lane_value(incl, kWave - 1);
   if (!token) return -1;
-  const uint64_t over = __ballot(w > 0.0 && incl > (double)u * S), some = __ballot(w > 0.0);
+  const uint64_t over = __ballot(w > kFdNothing && incl > (double)u * S), some = __ballot(w > kFdNothing);
   return lane_value(id, over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)some));
 }
 
@@ -572,7 +583,7 @@ __device__ __forceinline__ int fd_draw(FdShared& s, const FdRow<T>& row, const d
   int pick = -1, last = -1;
   for (int g = g0; g < g1; ++g) {
     const double w = seg[g];
-    if (w > 0.0) {
+    if (w > kFdNothing) {
       last = g;
       last_at = run;
       if (pick < 0 && run + w > target) {
@@ -609,7 +620,7 @@ __device__ __forceinline__ int fd_draw(FdShared& s, const FdRow<T>& row, const d
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       here += w[i];
-      if (w[i] > 0.0) {
+      if (w[i] > kFdNothing) {
         tail = e + i;
         if (first < 0 && here > target) first = tail;
       }
@@ -630,8 +641,8 @@ __device__ __forceinline__ int fd_draw(FdShared& s, const FdRow<T>& row, const d
   return y < 0 ? end : y;
 }
 
-// Masses put into bins of their distance from the maximum (bins to a unit of
-// FdExp), past the last into tail.
+// Masses put into bins of their distance from the maximum (so many bins to a unit
+// of (m - z) / T), past the last into tail.
 template <int N>
 __device__ __forceinline__ void fd_spread(FdShared& s, const FdExp& weight, const float (&v)[N],
                                           double unit, double bins, int nbin,
@@ -640,8 +651,8 @@ __device__ __forceinline__ void fd_spread(FdShared& s, const FdExp& weight, cons
   double b[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const double x = weight.units(v[i]);
-    w[i] = fd_fixed(weight.of_units(x), unit);
+    const double x = weight.arg(v[i]);
+    w[i] = fd_fixed(weight.of(x), unit);
     b[i] = -x * bins;
   }
 #pragma unroll
@@ -668,7 +679,7 @@ __device__ __forceinline__ void fd_sample(FdShared& s, const FdRow<T>& row, cons
   const int n = min(chunks, kChunks);
   for (int i = t; i < kFdSampleBins; i += kFdPlanThreads) s.mass[i] = 0;
   __syncthreads();
-  const double per = kFdSampleBins / width, bins = per / SPECV_EXP64_INV_L;
+  const double per = kFdSampleBins / width;
   unsigned long long tail = 0;
   constexpr int kSweeps = kChunks * kChunk / kFdPlanThreads;
   float v[kSweeps][N];
@@ -679,7 +690,7 @@ __device__ __forceinline__ void fd_sample(FdShared& s, const FdRow<T>& row, cons
     row.load(c < n ? q : row.vecs(), v[i]);          // past the row: -inf
   }
 #pragma unroll
-  for (int i = 0; i < kSweeps; ++i) fd_spread(s, weight, v[i], unit, bins, kFdSampleBins, tail);
+  for (int i = 0; i < kSweeps; ++i) fd_spread(s, weight, v[i], unit, per, kFdSampleBins, tail);
   unsigned long long all;
   fd_block_scan<kWaves>(s, tail, all);
   // thread t owns bins top - 2 t and the one below: sums from the far end
@@ -690,7 +701,7 @@ __device__ __forceinline__ void fd_sample(FdShared& s, const FdRow<T>& row, cons
   const double scale = (double)chunks / n / unit;
   uint32_t low = 0, high = 0;                        // ~b of lo, b + 1 of hi
   auto look = [&](int b, unsigned long long sum) {   // tokens from bin b on
-    const double M = scale * (double)sum, q = scale * unit * exp64(-b / per, s.tbl);
+    const double M = scale * (double)sum, q = scale * unit * weight.of(-b / per);
     const double off = 4.0 * sqrt(q * M) + 8.0 * q;
     if (M + off <= B) low = max(low, ~(uint32_t)b);
     if (M - off >= B) high = max(high, (uint32_t)b + 1u);
@@ -717,7 +728,7 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
   const double* ssum = a.ssum + (size_t)r * a.nseg;
   const float u = a.tokens ? a.u[(size_t)b * a.usb + (size_t)l * a.usl] : 0.f;
   const FdParams f = fd_params(a.f, b);
-  exp64_stage_table<kFdPlanThreads>(s.tbl);
+  fd_stage_table<kFdPlanThreads>(s.tbl);
   const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
 
   // the row's largest logit; NaN or +inf anywhere shows as the largest key
@@ -847,7 +858,7 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_collect_kernel(FdArgs a
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int items = *a.nitem;
   if ((int)blockIdx.x * kWaves >= items) return;
-  exp64_stage_table<kFdStatThreads>(tbl);
+  fd_stage_table<kFdStatThreads>(tbl);
   __syncthreads();
   for (int i = blockIdx.x * kWaves + wave; i < items; i += gridDim.x * kWaves) {
     const uint2 item = a.items[i];
@@ -947,7 +958,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
   const float4* gmax = a.gmax + (size_t)r * a.nseg;
   const double* ssum = a.ssum + (size_t)r * a.nseg;
   const uint2* part = a.part + (size_t)r * a.nseg;
-  if (t < SPECV_EXP64_N) s.tbl[t] = kExp64Table[t];
+  fd_stage_table<kFdThreads>(s.tbl);
   const FdRow<T> row(static_cast<const T*>(a.z) + (size_t)b * a.zsb + (size_t)l * a.zsl, a.V);
   const FdExp weight(m, invT, s.tbl);
   auto fixed = [&](float z) { return fd_fixed(weight(z), unit); };
@@ -1154,7 +1165,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
   const int nv = row.vecs();
   const float u = a.tokens ? a.u[(size_t)b * a.usb + (size_t)l * a.usl] : 0.f;
   const FdParams f = fd_params(a.f, b);
-  if (t < SPECV_EXP64_N) s.tbl[t] = kExp64Table[t];
+  fd_stage_table<kFdThreads>(s.tbl);
   float big = -INFINITY;
   bool fine = true;
 #pragma unroll 4
@@ -1264,14 +1275,14 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
                                                fixed).low;
     } else if (by_p && !by_k) {
       const double width = 1e-6 - log((1.0 - (double)f.p) / a.V);
-      const double per = kFdBins / width, bins = per / SPECV_EXP64_INV_L;
+      const double per = kFdBins / width;
       for (int i = t; i < kFdBins; i += kFdThreads) s.mass[i] = 0;
       __syncthreads();
       unsigned long long tail = 0, all, rest;
       for (int q = t; q < nv; q += kFdThreads) {
         float v[N];
         unpack(kept[q], v, T{});
-        fd_spread(s, weight, v, unit, bins, kFdBins, tail);
+        fd_spread(s, weight, v, unit, per, kFdBins, tail);
       }
       fd_block_scan<kFdWaves>(s, tail, rest);        // (its barriers serve the bins too)
       const unsigned long long x0 = s.mass[2 * t], x1 = s.mass[2 * t + 1];
@@ -1286,7 +1297,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
       // its logits
       const int at = (int)found - 1;
       auto in_bin = [&](float z) {
-        const double bin = -weight.units(z) * bins;
+        const double bin = -weight.arg(z) * per;
         return bin >= at && bin < at + 1;
       };
       // (a cheap look first: their range, with room for the edges' rounding)
@@ -1362,7 +1373,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
       int pick = -1, last = -1;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        if (w[i] > 0.0) {
+        if (w[i] > kFdNothing) {
           last = lane * kPer + i;
           last_at = run;
           if (pick < 0 && run + w[i] > target) {
@@ -1391,7 +1402,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           here += x[j];
-          if (x[j] > 0.0) {
+          if (x[j] > kFdNothing) {
             tail = row.first(q) + j;
             if (first < 0 && here > target) first = tail;
           }

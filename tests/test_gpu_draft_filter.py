@@ -129,6 +129,21 @@ def test_uniforms_at_the_ends():
             check(z, u, *f, probs, tok)
 
 
+def test_weights_that_vanish():
+    # far below the largest a weight counts as nothing, also at u = 0
+    z = torch.zeros(6, 40000)
+    z[:, 35000] = 100.0
+    z[:, 35010] = 99.0
+    u = torch.tensor([0.0, 2.0 ** -24, 0.5, 0.999, 0.0, 1 - 2.0 ** -24])
+    for V in (36000, 40000, 20):
+        zz = z[:, 35000:35020].contiguous() if V == 20 else z[:, :V].contiguous()
+        if V == 20:
+            zz = torch.cat([torch.zeros(6, 10), zz], 1)
+        for f in ((0.1, 0, 1.0, 0.0), (0.01, 0, 0.9999, 0.0), (0.1, 5, 1.0, 0.0), (0.1, 300, 1.0, 0.0)):
+            probs, tok = both(zz, u, *f)
+            check(zz, u, *f, None, tok)
+
+
 def test_masked_and_bad_rows():
     V = 3000
     z = logits(12, V, 8)
