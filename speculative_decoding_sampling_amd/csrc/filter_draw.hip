@@ -152,18 +152,33 @@ __device__ __forceinline__ bool fd_wants_sums(const FdParams& f, int V) {
   return f.ok && f.T > 0.f && (f.k == 0 || f.k >= V) && (f.p < 1.f || f.mp == 0.f);
 }
 
-// Weights exp((z - m) / T), at most 1: exp64.h's method and table, whose entries
-// stand in LDS with their index taken from the exponent's place, so that adding
-// k there leaves 2^(k / N) in one operation.  What would be below e^-700 stays
-// there and counts as nothing in a draw; -inf is told apart by whoever sums.
+// Weights exp((z - m) / T), at most 1: exp64.h's method and table.  The entries
+// have their index taken from the exponent's place, so that adding k there leaves
+// 2^(k / N) in one operation.  What would be below e^-700 stays there and counts as
+// nothing in a draw; -inf is told apart by whoever sums.
 constexpr double kFdNothing = 1e-290;
+template <int BITS>                                  // of the 9 of the table's index
 __device__ __forceinline__ double fd_table_entry(int i) {
-  const double v = kExp64Table[i];
-  return __hiloint2double(__double2hiint(v) - (i << (20 - SPECV_EXP64_LOG2N)), __double2loint(v));
+  const double v = kExp64Table[i << (SPECV_EXP64_LOG2N - BITS)];
+  return __hiloint2double(__double2hiint(v) - (i << (20 - BITS)), __double2loint(v));
 }
+
+// The sum of the weights at or above tau, finite.  No branches: the weights'
+// chains of dependent operations and table reads overlap.
+template <typename E, int N>
+__device__ __forceinline__ double fd_sum(const E& weight, const float (&v)[N], float tau) {
+  double w[N], s = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = weight(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) s += v[i] >= tau && v[i] > -INFINITY ? w[i] : 0.0;
+  return s;
+}
+
+// With the table of 512 in LDS.
 template <int NT>
 __device__ __forceinline__ void fd_stage_table(double* tbl) {
-  for (int i = threadIdx.x; i < SPECV_EXP64_N; i += NT) tbl[i] = fd_table_entry(i);
+  for (int i = threadIdx.x; i < SPECV_EXP64_N; i += NT) tbl[i] = fd_table_entry<SPECV_EXP64_LOG2N>(i);
 }
 struct FdExp {
   double m, invT;
@@ -184,16 +199,30 @@ struct FdExp {
     return fma(tj, r * q, tj);
   }
   __device__ __forceinline__ double operator()(float z) const { return of(arg(z)); }
-  // The sum of those at or above tau, finite.  No branches: the weights' chains
-  // of dependent operations and table reads overlap.
-  template <int N>
-  __device__ __forceinline__ double sum(const float (&v)[N], float tau) const {
-    double w[N], s = 0.0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = (*this)(v[i]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) s += v[i] >= tau && v[i] > -INFINITY ? w[i] : 0.0;
-    return s;
+};
+
+// With every eighth entry of the table, one in each lane of a wave, read across
+// lanes: nothing to stage and no barrier, one degree more (truncation r^5 / 120 <
+// 4e-14).  All lanes call it together: a lane that is off gives zeros.
+struct FdWaveExp {
+  double m, invT;
+  int lo, hi;
+  __device__ __forceinline__ FdWaveExp(double m, double invT) : m(m), invT(invT) {
+    const double v = fd_table_entry<6>(threadIdx.x % kWave);
+    lo = __double2loint(v);
+    hi = __double2hiint(v);
+  }
+  __device__ __forceinline__ double operator()(float z) const {
+    const double x = fmax(((double)z - m) * invT, -700.0);
+    const double t = fma(x, SPECV_EXP64_INV_L / 8, SPECV_EXP64_SHIFT);
+    const double r = fma(-(t - SPECV_EXP64_SHIFT), SPECV_EXP64_L * 8, x);
+    double q = fma(r, 1.0 / 24, SPECV_EXP64_C3);
+    q = fma(r, q, 0.5);
+    q = fma(r, q, 1.0);
+    const int k = __double2loint(t);                 // (lane k % 64)
+    const double tj = __hiloint2double(__builtin_amdgcn_ds_bpermute(k << 2, hi) + (k << 14),
+                                       __builtin_amdgcn_ds_bpermute(k << 2, lo));
+    return fma(tj, r * q, tj);
   }
 };
 
@@ -206,11 +235,13 @@ __device__ __forceinline__ unsigned long long fd_fixed(double w, double unit) {
   return (unsigned long long)__double_as_longlong(fma(w, unit, 4503599627370496.0)) & 0xfffffffffffffull;
 }
 
-// A row's groups: one wave a segment.
+// A row's groups: one wave a segment.  Without sums it reads 5.8 TB/s (27 us for
+// 156 MB); float64 weights of all tokens add 10 us there.  (A table staged for each
+// workgroup cost 7 us more; workgroups that stay and fetch ahead, or neighbouring
+// ones on different rows, read slower.)
 template <typename T>
 __global__ __launch_bounds__(kFdStatThreads) void filter_stats_kernel(FdArgs a, int nblk) {
   constexpr int N = FdRow<T>::N;
-  __shared__ double tbl[SPECV_EXP64_N];
   const int r = blockIdx.x / nblk, b = r / a.L, l = r % a.L;
   const int lane = threadIdx.x % kWave;
   const int g = (blockIdx.x % nblk) * (kFdStatThreads / kWave) +
@@ -227,10 +258,6 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_stats_kernel(FdArgs a, 
   }
   const FdParams f = fd_params(a.f, b);
   const bool sums = fd_wants_sums(f, a.V);
-  if (sums) {
-    fd_stage_table<kFdStatThreads>(tbl);
-    __syncthreads();
-  }
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.nitem = 0;     // for the plans, which follow
   if (g >= a.nseg) return;
   float top[kFdGroups], m = -INFINITY;
@@ -251,7 +278,7 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_stats_kernel(FdArgs a, 
   }
   double w = 0.0;
   if (sums && m > -INFINITY) {
-    const FdExp e(m, 1.0 / (double)f.T, tbl);
+    const FdWaveExp e(m, 1.0 / (double)f.T);
 #pragma unroll
     for (int j = 0; j < kFdGroups; ++j) {
       float v[N];
@@ -853,13 +880,10 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
 template <typename T>
 __global__ __launch_bounds__(kFdStatThreads) void filter_collect_kernel(FdArgs a) {
   constexpr int N = FdRow<T>::N, kWaves = kFdStatThreads / kWave;
-  __shared__ double tbl[SPECV_EXP64_N];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int items = *a.nitem;
   if ((int)blockIdx.x * kWaves >= items) return;
-  fd_stage_table<kFdStatThreads>(tbl);
-  __syncthreads();
   for (int i = blockIdx.x * kWaves + wave; i < items; i += gridDim.x * kWaves) {
     const uint2 item = a.items[i];
     const int r = (int)item.x, b = r / a.L, l = r % a.L, g = (int)(item.y >> 4);
@@ -872,10 +896,10 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_collect_kernel(FdArgs a
     const uint32_t over = fd_reach(a.gmax[at], hi);
     double w = 0.0;
     if (over) {
-      const FdExp weight(plan->m, plan->invT, tbl);
+      const FdWaveExp weight(plan->m, plan->invT);
 #pragma unroll
       for (int j = 0; j < kFdGroups; ++j)
-        if (over >> j & 1u) w += weight.sum(v[j], hi);
+        if (over >> j & 1u) w += fd_sum(weight, v[j], hi);
       w = wave_sum(w);
     }
     uint32_t n = 0, from = 0;
@@ -1044,7 +1068,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
       fd_load(row, pick, lane, v);
       double w = 0.0;
 #pragma unroll
-      for (int j = 0; j < kFdGroups; ++j) w += weight.sum(v[j], tau);
+      for (int j = 0; j < kFdGroups; ++j) w += fd_sum(weight, v[j], tau);
       w = wave_sum(w);
       if (lane == 0) seg[pick >> 4] = w;
     }
@@ -1353,7 +1377,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
       bool some = false;
 #pragma unroll
       for (int j = 0; j < N; ++j) some = some || (v[j] >= tau && v[j] > -INFINITY);
-      if (__any(some)) w = wave_sum(weight.sum(v, tau));
+      if (__any(some)) w = wave_sum(fd_sum(weight, v, tau));
       if (lane == 0) o.group[g] = w;
     }
     __syncthreads();
