@@ -359,6 +359,11 @@ template <typename T>
 __device__ __forceinline__ float fd_unkey(uint32_t k) {
   return unkey(sizeof(T) == 2 ? k << 16 : k);
 }
+// The logit of a key.
+template <typename T>
+__device__ __forceinline__ float fd_value(uint32_t k) {
+  return unkey(sizeof(T) == 4 ? k : k < 0x8000u ? k << 16 | 0xffffu : k << 16);
+}
 template <typename T>
 constexpr uint32_t kFdLowest = sizeof(T) == 2 ? (kNegInfKey >> 16) + 1 : kNegInfKey + 1;
 
@@ -436,8 +441,10 @@ struct FdFound {
 // the keys of the bracket [lo, hi] into bins by count, and by mass where that is
 // what the target is about, finds the bin where the running sum from the top
 // reaches the target and goes on inside it, until it holds one value (or one key:
-// ties go together).  A BOUND takes one round.
-template <int THREADS, bool MASS, bool BOUND, typename Each, typename W>
+// ties go together).  A BOUND takes one round.  Where a bin is one key, its mass is
+// its count times that key's weight: bfloat16 logits share few keys, whose masses
+// would all be added at the same places.
+template <int THREADS, bool MASS, bool BOUND, typename T, typename Each, typename W>
 __device__ __forceinline__ FdFound fd_search(FdShared& s, uint32_t lo, uint32_t hi,
                                              unsigned long long above, double target, Each each,
                                              W weight) {
@@ -449,22 +456,25 @@ __device__ __forceinline__ FdFound fd_search(FdShared& s, uint32_t lo, uint32_t 
     const int sh = max(32 - __clz((int)((hi - lo) | 1u)) - kBits, 0);
     for (int i = t; i < kBins; i += THREADS) {
       s.count[i] = 0;
-      if (MASS) s.mass[i] = 0;
+      if (MASS && sh) s.mass[i] = 0;
     }
     __syncthreads();
     each([&](uint32_t key, float z) {
       if (key >= lo && key <= hi) {
         const int b = (int)((key - lo) >> sh);
         atomicAdd(&s.count[b], 1u);
-        if (MASS) atomicAdd(&s.mass[b], weight(z));
+        if (MASS && sh) atomicAdd(&s.mass[b], weight(z));
       }
     });
     __syncthreads();
     // thread t owns bins top - 2 t and the one below: running sums from the top
     const int b0 = kBins - 1 - 2 * t, b1 = b0 - 1;
     const uint32_t c0 = s.count[b0], c1 = s.count[b1];
-    const unsigned long long x0 = MASS ? s.mass[b0] : c0;
-    const unsigned long long x1 = MASS ? s.mass[b1] : c1;
+    unsigned long long x0 = c0, x1 = c1;
+    if (MASS) {
+      x0 = sh ? s.mass[b0] : c0 ? c0 * weight(fd_value<T>(lo + b0)) : 0ull;
+      x1 = sh ? s.mass[b1] : c1 ? c1 * weight(fd_value<T>(lo + b1)) : 0ull;
+    }
     const unsigned long long incl = wave_incl_scan_u64(x0 + x1);
     if (lane == kWave - 1) s.wave_u64[wave] = incl;
     __syncthreads();
@@ -826,7 +836,7 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
               put(fd_key<T>(x.w), x.w);
             }
           };
-          const FdFound k = fd_search<kFdPlanThreads, false, true>(
+          const FdFound k = fd_search<kFdPlanThreads, false, true, T>(
               s, kFdLowest<T>, fd_key<T>(m), 0, (double)f.k, maxima, [](float) { return 0ull; });
           if (k.reached) plan.lo = fd_unkey<T>(k.low);
         }
@@ -1000,11 +1010,10 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
   if (by_k || by_p) {
     FdSource<T> src = {row, picks, 0u, list, n, true};
     auto each = [&](auto put) { src.each([&](float z) { put(fd_key<T>(z), z); }); };
-    const uint32_t top = fd_key<T>(m);
-    auto search = [&](float from, unsigned long long above) -> FdFound {
+    auto search = [&](float from, uint32_t top, unsigned long long above) -> FdFound {
       FdFound k = {from > -INFINITY ? fd_key<T>(from) : kFdLowest<T>, true};
       if (by_k)
-        k = fd_search<kFdThreads, false, false>(s, k.low, top, 0, (double)f.k, each,
+        k = fd_search<kFdThreads, false, false, T>(s, k.low, top, 0, (double)f.k, each,
                                                 [](float) { return 0ull; });
       if (by_p) {
         double target = (double)f.p * plan.Z * unit;
@@ -1016,14 +1025,15 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
           fd_block_scan<kFdWaves>(s, sum, all);
           target = (double)f.p * (double)all;
         }
-        k = fd_search<kFdThreads, true, false>(s, k.low, top, above, target, each, fixed);
+        k = fd_search<kFdThreads, true, false, T>(s, k.low, top, above, target, each, fixed);
       }
       k.reached = k.reached || by_k;
       return k;
     };
     FdFound k = {0u, false};
     if (whole && (by_k || high < (double)f.p * plan.Z)) {
-      k = search(plan.lo, (unsigned long long)__double2ll_rn(high * unit));
+      // (the range that the list covers, so that its bins are fine)
+      k = search(plan.lo, fd_key<T>(fminf(plan.hi, m)), (unsigned long long)__double2ll_rn(high * unit));
       // not reached: the threshold lies below the bracket, and below min-p's if
       // the bracket starts there
       if (!k.reached && plan.lo == plan.tau)
@@ -1035,7 +1045,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
       __syncthreads();
       src.npick = fd_pick(s, picks, gmax, a.nseg, from);
       src.listed = whole = false;
-      k = search(from, 0ull);
+      k = search(from, fd_key<T>(m), 0ull);
     }
     tau = fmaxf(tau, fd_unkey<T>(k.low));
   }
@@ -1248,7 +1258,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
     if (by_k) {
       if (f.k <= kFdThreads) {
         // at least k tokens reach the k-th largest of the threads' maxima
-        const FdFound k = fd_search<kFdThreads, false, true>(
+        const FdFound k = fd_search<kFdThreads, false, true, T>(
             s, low, high, 0, (double)f.k, [&](auto add) { add(fd_key<T>(big), big); },
             [](float) { return 0ull; });
         if (k.reached) low = k.low;
@@ -1286,7 +1296,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
         }
       }
       if (!done)
-        low = fd_search<kFdThreads, false, false>(s, low, high, 0, (double)f.k, each,
+        low = fd_search<kFdThreads, false, false, T>(s, low, high, 0, (double)f.k, each,
                                                   [](float) { return 0ull; }).low;
     }
     if (by_p && by_k && !done) {
@@ -1295,7 +1305,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
         if (key >= low) sum += fixed(z);
       });
       fd_block_scan<kFdWaves>(s, sum, all);
-      low = fd_search<kFdThreads, true, false>(s, low, high, 0, (double)f.p * (double)all, each,
+      low = fd_search<kFdThreads, true, false, T>(s, low, high, 0, (double)f.p * (double)all, each,
                                                fixed).low;
     } else if (by_p && !by_k) {
       const double width = 1e-6 - log((1.0 - (double)f.p) / a.V);
@@ -1354,7 +1364,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
         }
         low = ~wave_max_u32(lane < n && (double)over < target ? ~key : 0u);
       } else {
-        low = fd_search<kFdThreads, true, false>(
+        low = fd_search<kFdThreads, true, false, T>(
                   s, k0, k1, above, target,
                   [&](auto add) {
                     each([&](uint32_t key, float z) {
