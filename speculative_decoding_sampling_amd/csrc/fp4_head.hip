@@ -264,7 +264,8 @@ template <int MT, bool H8, typename O>
 struct Fp4Tile {
   static constexpr int kRows = MT * 32;
   static constexpr int kBuf = kRows * kF4RowBytes;
-  static constexpr int kBytes = 2 * kBuf > HeadStore<O>::kBytes ? 2 * kBuf : HeadStore<O>::kBytes;
+  static constexpr int kTrBytes = HeadStore<MT, O>::kBytes;
+  static constexpr int kBytes = 2 * kBuf > kTrBytes ? 2 * kBuf : kTrBytes;
   static constexpr int kSteps = H8 ? 2 : 4;        // of a run
   static constexpr int kRing = MT <= 1 || H8 ? 4 : 2;   // runs of weights in registers
 };
@@ -421,7 +422,6 @@ __device__ __forceinline__ void fp4_tile(uint8_t* lds, uint32_t (&lsc)[2][2 * kF
           else both(std::integral_constant<int, 3>{});
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
     store_h((I + 1) % 2, kb + 1);
   };

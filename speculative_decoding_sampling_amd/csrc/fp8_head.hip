@@ -297,7 +297,7 @@ template <int MT, typename O>
 struct Fp8Tile {
   static constexpr int kRows = MT * 32;
   static constexpr int kBuf = kRows * kFp8Block;
-  static constexpr int kTrBytes = HeadStore<O>::kBytes;
+  static constexpr int kTrBytes = HeadStore<MT, O>::kBytes;
   static constexpr int kBytes = 2 * kBuf > kTrBytes ? 2 * kBuf : kTrBytes;
   static constexpr int kRing = MT <= 2 ? 4 : 2;              // runs of weights in registers
 };

@@ -2,6 +2,8 @@
 // product loop and the way of a tile's logits to memory.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "fp8.h"
 
@@ -50,21 +52,25 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// The LDS that a tile's logits leave through: 32 rows of bfloat16 or 16 of
-// float32 at a time.
-template <typename O>
+// The LDS that a tile's logits leave through: up to 128 rows of bfloat16 or 64 of
+// float32 at a time, 70 KB (two workgroups a CU have 80 each), so that few barriers
+// part the stores.  At 1152 x 152064 x 4096 of 4-bit weights and states this takes
+// 469 us; 32 rows at a time took 479, and no stores at all 435.  At 8-bit states,
+// bound by the products, both take the same.
+template <int MT, typename O>
 struct HeadStore {
   static constexpr int kStride = kTileVocab + 16 / (int)sizeof(O);
-  static constexpr int kRows = 64 / (int)sizeof(O);
-  static constexpr int kBytes = kRows * kStride * (int)sizeof(O);
+  static constexpr int kMost = 8 / (int)sizeof(O);         // 32-row steps of a pass
+  static constexpr int kSteps = MT < kMost ? MT : kMost;
+  static constexpr int kBytes = 32 * kSteps * kStride * (int)sizeof(O);
 };
 
 // A tile's logits, by its four waves, to rows m0 .. and ids 256 tile ..; lds is
-// free at the call (HeadStore<O>::kBytes of it are used).
+// free at the call (HeadStore<MT, O>::kBytes of it are used).
 template <int MT, typename O>
 __device__ __forceinline__ void head_store(uint8_t* lds, const HeadF32x16 (&acc)[2][MT], int tile,
                                            int m0, int M, int V, O* __restrict__ out) {
-  constexpr int kTrStride = HeadStore<O>::kStride, kTrRows = HeadStore<O>::kRows;
+  constexpr int kTrStride = HeadStore<MT, O>::kStride, kSteps = HeadStore<MT, O>::kSteps;
   const int tid = threadIdx.x, lane = tid % kWave, h = lane / 32, l32 = lane % 32;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   // acc[a][t][r] is the logit of row 32 t + l32 of the block and vocabulary id
@@ -79,54 +85,61 @@ __device__ __forceinline__ void head_store(uint8_t* lds, const HeadF32x16 (&acc)
   constexpr int kVec = 16 / sizeof(O);
   const bool whole = V % kVec == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
   O* tr = reinterpret_cast<O*>(lds);
+  auto pass = [&](auto first) {
+    constexpr int t0 = decltype(first)::value, kT = kSteps < MT - t0 ? kSteps : MT - t0;
+    constexpr int kPassRows = 32 * kT, r0 = t0 * 32;         // its rows, the first in the block
+    // float32 in two halves of the lanes: written by all at once, the compiler
+    // spills the accumulators (52 to 208 registers)
+    constexpr int kHalves = sizeof(O) / 2;
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+    for (int i = 0; i < kT * kHalves; ++i) {
+      const int t = i / kHalves;
+      if (kHalves > 1 && l32 / 16 != i % kHalves) continue;
+      O* row = tr + (t * 32 + l32) * kTrStride + vb;
 #pragma unroll
-    for (int part = 0; part < 32 / kTrRows; ++part) {
-      const int r0 = t * 32 + part * kTrRows;               // first row of the part in the block
-      if (32 == kTrRows || l32 / kTrRows == part) {
-        O* row = tr + (l32 % kTrRows) * kTrStride + vb;
+      for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) head_put4(row + 32 * a + 8 * q, acc[a][t], 4 * q);
-      }
-      lds_barrier();
-      if (whole) {
-#pragma unroll
-        for (int i = 0; i < kTrRows * kTileVocab / kVec / kHeadThreads; ++i) {
-          const int p = tid + i * kHeadThreads, row = p / (kTileVocab / kVec);
-          const int c = p % (kTileVocab / kVec) * kVec;
-          if (m0 + r0 + row < M && c < nv)
-            *reinterpret_cast<uint4*>(out + (size_t)(m0 + r0 + row) * V + v0 + c) =
-                *reinterpret_cast<const uint4*>(tr + row * kTrStride + c);
-        }
-      } else {
-        constexpr int kLog = 4 / sizeof(O);                  // logits of a 4-byte store
-#pragma unroll
-        for (int i = 0; i < kTrRows * kTileVocab / kLog / kHeadThreads; ++i) {
-          const int p = tid + i * kHeadThreads, row = p / (kTileVocab / kLog);
-          if (m0 + r0 + row >= M) continue;
-          O* dst = out + (size_t)(m0 + r0 + row) * V + v0;
-          const O* src = tr + row * kTrStride;
-          if constexpr (sizeof(O) == 4) {
-            const int c = p % kTileVocab;
-            if (c < nv) dst[c] = src[c];
-          } else {
-            // aligned words start at the row's first logit or its second; a
-            // first or last logit without a partner is stored alone
-            const int odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
-            const int c = odd + 2 * (p % (kTileVocab / 2));
-            if (odd && c == 1) dst[0] = src[0];
-            if (c + 1 < nv)
-              *reinterpret_cast<uint32_t*>(dst + c) = (uint32_t)src[c] | (uint32_t)src[c + 1] << 16;
-            else if (c < nv)
-              dst[c] = src[c];
-          }
-        }
-      }
-      lds_barrier();
+        for (int q = 0; q < 4; ++q) head_put4(row + 32 * a + 8 * q, acc[a][t0 + t], 4 * q);
     }
+    lds_barrier();
+    if (whole) {
+#pragma unroll 4
+      for (int i = 0; i < kPassRows * kTileVocab / kVec / kHeadThreads; ++i) {
+        const int p = tid + i * kHeadThreads, row = p / (kTileVocab / kVec);
+        const int c = p % (kTileVocab / kVec) * kVec;
+        if (m0 + r0 + row < M && c < nv)
+          *reinterpret_cast<uint4*>(out + (size_t)(m0 + r0 + row) * V + v0 + c) =
+              *reinterpret_cast<const uint4*>(tr + row * kTrStride + c);
+      }
+    } else {
+      constexpr int kLog = 4 / sizeof(O);                  // logits of a 4-byte store
+#pragma unroll 4
+      for (int i = 0; i < kPassRows * kTileVocab / kLog / kHeadThreads; ++i) {
+        const int p = tid + i * kHeadThreads, row = p / (kTileVocab / kLog);
+        if (m0 + r0 + row >= M) continue;
+        O* dst = out + (size_t)(m0 + r0 + row) * V + v0;
+        const O* src = tr + row * kTrStride;
+        if constexpr (sizeof(O) == 4) {
+          const int c = p % kTileVocab;
+          if (c < nv) dst[c] = src[c];
+        } else {
+          // aligned words start at the row's first logit or its second; a
+          // first or last logit without a partner is stored alone
+          const int odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
+          const int c = odd + 2 * (p % (kTileVocab / 2));
+          if (odd && c == 1) dst[0] = src[0];
+          if (c + 1 < nv)
+            *reinterpret_cast<uint32_t*>(dst + c) = (uint32_t)src[c] | (uint32_t)src[c + 1] << 16;
+          else if (c < nv)
+            dst[c] = src[c];
+        }
+      }
+    }
+    lds_barrier();
+  };
+  pass(std::integral_constant<int, 0>{});
+  if constexpr (MT > kSteps) pass(std::integral_constant<int, kSteps>{});
+  static_assert(MT <= 2 * kSteps, "two passes at most");
 }
 
 }  // namespace specv
