@@ -540,12 +540,36 @@ hipError_t fp4_skinny(const Fp4Args& a, O* out) {
 
 constexpr double kFp4CacheBytes = 256.0 * (1 << 20);
 
-// Which product: 0 the skinny one, MT = 1..4 row blocks of at most 32 MT hidden
-// rows.  At 32 rows the skinny one takes 99 us of 128256 x 4096, a tile 52.
-int fp4_choice(int M, int D, int V, bool h8, bool exact) {
-  if (M <= 16) return 0;
-  const int mt = (M + 31) / 32;
-  return exact ? (mt < 3 ? mt : 3) : mt < 4 ? mt : 4;
+// Which product: 0 the skinny one, 1 .. 4 tiles of at most 32 times as many
+// hidden rows.
+//
+// The skinny one has eight times the workgroups, each a chain an eighth as long,
+// but reads the weights once for every 32 rows.  It is taken where its
+// workgroups (an empty row block counts half) are at most four a CU for 64 rows,
+// two for more: at D = 4096 and 8-bit states 8000 x 64 takes 14.6 us and by tiles
+// 20.2, 20001 x 17 14.8 and 22.8; beyond, 20001 x 64 31.0 and 24.2, 8000 x 100
+// 22.4 and 20.3, 128256 x 1 52.3 and 49.2, 128256 x 32 98 and 52.
+//
+// Among tiles: a CU does its share of them at the pace of one, whose time grows
+// as 2 D for the weights and D + 640 for each 32 rows and their logits.  At
+// 32000 x 4096 and 160 rows 32, 64, 96 and 128 rows take 39, 34, 30 and 30 us, at
+// 128256 and 100 rows 100, 83, 85 and 70, at 20001 and 64 rows 24, 30, 30 and 30;
+// over 250 sizes, M from 1 to 1152, the rule's choice takes 1.4 % more than the
+// best one (geometric mean; 30 % at most, 20001 x 1024 with 200 rows).
+int fp4_choice(int M, int D, int V, bool exact) {
+  constexpr long long kCus = 256;
+  const long long groups = fp4_groups(V), blocks = (M + 31) / 32;
+  if (groups * blocks <= 2 * kCus || (M <= 64 && groups * (32 * blocks + M) <= 64 * 4 * kCus))
+    return 0;
+  const long long tiles = ((long long)V + kTileVocab - 1) / kTileVocab;
+  int best = 1;
+  long long least = 0;
+  for (int mt = 1; mt <= (exact ? 3 : 4); ++mt) {
+    const long long work = tiles * ((M + 32 * mt - 1) / (32 * mt));
+    const long long cost = (work + kCus - 1) / kCus * (2 * D + mt * (D + 640));
+    if (mt == 1 || cost < least) best = mt, least = cost;
+  }
+  return best;
 }
 
 template <bool ONCE, bool H8, typename O>
@@ -559,7 +583,7 @@ hipError_t fp4_run(const Fp4Args& a, int choice, O* out) {
 }
 template <bool H8, typename O>
 hipError_t fp4_head(const Fp4Args& a, O* out) {
-  const int choice = fp4_choice(a.M, a.D, a.V, H8, kFp4Exact<H8, O>);
+  const int choice = fp4_choice(a.M, a.D, a.V, kFp4Exact<H8, O>);
   const int rows = choice == 0 ? 32 : 32 * choice;
   return a.M <= rows && (double)a.V * a.D / 2 > kFp4CacheBytes ? fp4_run<true, H8>(a, choice, out)
                                                                   : fp4_run<false, H8>(a, choice, out);
