@@ -2,7 +2,9 @@
 
 Tokens must equal the reference's draw unless its t lies within 1e-10 of the mass
 from another token, or a top-p or min-p decision within 1e-9 of the other
-outcome (n weights held to 2^-46 are off by n 2^-47 at most, 1e-9 at n = 150000).
+outcome, as a share of the mass.  (n weights held to whole multiples of 2^-s, s = 62 -
+ceil(log2 n), are off by n 2^-(s+1) at most, at n = 152064 4e-9 of the largest
+weight, in rows whose mass is 5 and more times as large.)
 A probability is exp2(f) 2^k / S: the hardware's exp2 within 1 ulp (2^-23), f, a
 float32 in [-1/2, 1/2] rounded once (2^-26), the sum's reciprocal and the product
 (2^-24 each): below 2^-22 (1 + 1/8) of the value, and 2^-126 where it is subnormal;
