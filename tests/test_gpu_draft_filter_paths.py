@@ -136,3 +136,13 @@ def test_two_graphs_with_their_own_filters():
     for f, (probs, tok) in zip((a, b), want):
         f = tuple(x.cpu() if isinstance(x, torch.Tensor) else x for x in f)
         assert check(rows, u.view(-1).cpu(), *f, probs.view(B * L, V), tok.view(-1), L=L) <= 1
+
+
+def test_largest_vocabulary_of_float32():
+    V = 4194304
+    z = logits(2, V, 6, F32, 2.0, 40)
+    u = torch.tensor([0.3, 0.99999])
+    T, p = torch.tensor([1.0, 0.8]), torch.tensor([1.0, 0.9])
+    for k in (0, 40):
+        probs, tok = both(z, u, T, k, p, 0.0)
+        assert check(z, u, T, k, p, 0.0, probs, tok) <= 1
