@@ -139,8 +139,9 @@ typedef struct {
  *   p(v) = exp((z(v) - max z) / T) / S over the kept tokens, 0 elsewhere,
  * S their sum, and its token the first id whose running sum of the kept
  * weights exceeds u S (ids ascending, strict comparison, as specv_sample
- * draws; a weight below 1e-290 of the largest counts as nothing).  The kept set is decided on weights held to 2^-62 V of the largest (at
- * least 2^-51), the draw sums in float64; results do not change from run to run.
+ * draws; a weight below 1e-290 of the largest counts as nothing).  The kept set
+ * is decided on weights held to 2^-62 V of the largest (at least 2^-51), the
+ * draw sums in float64; results do not change from run to run.
  *
  *  logits      row l of request b starts at element b * stride_b + l *
  *              stride_l, V consecutive values of dtype, any alignment of an

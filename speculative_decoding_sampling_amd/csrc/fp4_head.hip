@@ -29,6 +29,7 @@ typedef int fp4_i32x8 __attribute__((ext_vector_type(8)));
 using fp4_f32x16 = HeadF32x16;
 typedef __bf16 fp4_bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 fp4_bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t fp4_word __attribute__((aligned(1), may_alias));   // scale bytes start anywhere
 
 constexpr int kF4Group = 32;                       // vocabulary rows of a packed group
 constexpr int kF4Step = 64;                        // columns of one product
@@ -366,7 +367,7 @@ __device__ __forceinline__ void fp4_tile(uint8_t* lds, uint32_t (&lsc)[2][2 * kF
 #pragma unroll
       for (int e = 0; e < 4; ++e) x.b[e] = hsrow[min(4 * g + e, nblock - 1)];
     } else {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(hsrow);
+      const fp4_word* p = reinterpret_cast<const fp4_word*>(hsrow);
 #pragma unroll
       for (int e = 0; e < 2; ++e) x.b[e] = p[min(2 * g + e, nblock / 4 - 1)];
     }

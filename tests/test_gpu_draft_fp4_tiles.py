@@ -60,6 +60,19 @@ def test_nan_stays_in_its_row_and_column(kind, dtype):
     assert torch.equal(got[~nan], want[~nan])
 
 
+@pytest.mark.parametrize("kind", [4, 8])
+@pytest.mark.parametrize("M,V", [(5, 3000), (150, 20001)])
+def test_scales_that_start_anywhere(kind, M, V):
+    D = 640
+    _, (q, s) = states(kind, M, D, 8)
+    packed = S.pack_fp4_lm_head(*dev4(*codes(V, D, -2, 0, 7)))
+    want = S.fp4_lm_head(q, s, packed)
+    for shift in (1, 2, 3):
+        room = torch.zeros(s.numel() + shift, dtype=torch.uint8, device=DEV)
+        room[shift:] = s.view(torch.uint8).flatten()
+        assert torch.equal(S.fp4_lm_head(q, room[shift:].view(s.shape).view(E8), packed), want)
+
+
 @pytest.mark.parametrize("V", [20000, 20001])
 def test_rows_around_the_logits_are_left(V):
     M, D = 150, 256
