@@ -838,8 +838,12 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
               put(fd_key<T>(x.w), x.w);
             }
           };
+          // (from the lowest of these, so that the bins are fine)
+          uint32_t least = 0;
+          maxima([&](uint32_t key, float x) { least = max(least, x > -INFINITY ? ~key : 0u); });
+          least = ~fd_block_max<kWaves>(s, least);
           const FdFound k = fd_search<kFdPlanThreads, false, true, T>(
-              s, kFdLowest<T>, fd_key<T>(m), 0, (double)f.k, maxima, [](float) { return 0ull; });
+              s, least, fd_key<T>(m), 0, (double)f.k, maxima, [](float) { return 0ull; });
           if (k.reached) plan.lo = fd_unkey<T>(k.low);
         }
         // top-p is a part of the whole top-k set's mass
@@ -1274,8 +1278,10 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
     if (by_k) {
       if (f.k <= kFdThreads) {
         // at least k tokens reach the k-th largest of the threads' maxima
+        // (from the lowest of these, so that the bins are fine)
+        const uint32_t least = ~fd_block_max<kFdWaves>(s, big > -INFINITY ? ~fd_key<T>(big) : 0u);
         const FdFound k = fd_search<kFdThreads, false, true, T>(
-            s, low, high, 0, (double)f.k, [&](auto add) { add(fd_key<T>(big), big); },
+            s, least, high, 0, (double)f.k, [&](auto add) { add(fd_key<T>(big), big); },
             [](float) { return 0ull; });
         if (k.reached) low = k.low;
         if (fd_key<T>(big) >= low)
