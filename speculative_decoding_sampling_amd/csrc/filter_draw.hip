@@ -51,6 +51,8 @@ constexpr int kFdPlanThreads = 512;
 constexpr int kFdCollectBlocks = 8 * 256;           // eight to a CU
 constexpr int kFdListCap = 16384;                   // collected logits of a row
 constexpr int kFdSampleBins = 2 * kFdPlanThreads;
+// The most LDS that a kernel asks for, of the 160 KB of a CU.
+constexpr int kFdLds = 159 * 1024;
 
 enum FdKind : int { kFdError = 0, kFdGreedy = 1, kFdDraw = 2 };
 // What is left to do for a row after its plan.
@@ -1196,15 +1198,18 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_probs_kernel(FdArgs a, 
 // over workgroups, as longer ones are, need four launches that take 35 us.
 constexpr int kFdOneGroups = 144;                   // groups of 64 vectors
 constexpr int kFdOneV = 32768;
+constexpr int kFdOneList = 512;                     // one to a thread
 
 struct FdOneShared {
   FdShared s;
   double group[kFdOneGroups];                       // their kept masses
-  uint2 few[kWave];                                 // a short list: logits and ids
+  uint16_t few[kFdOneList];                         // a list of places in the row
   double S;
   float tau;
 };
 static_assert(((kFdOneV + 6) / 4 + 63) / 64 <= kFdOneGroups, "every group has its mass");
+static_assert((sizeof(FdOneShared) + 15) / 16 * 16 + (kFdOneV + 6) / 4 * 16 <= kFdLds, "the row fits");
+static_assert(kFdOneList <= kFdThreads && kFdOneV + 14 < 65536, "a thread to an entry, 16 bits to a place");
 
 template <typename T, typename O>
 __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
@@ -1267,13 +1272,24 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
     const uint32_t high = fd_key<T>(m);
     tau = -INFINITY;
     if (f.mp > 0.f) tau = fd_min_p_threshold(m, f.T, weight, f.mp);
-    // logits put on a list of 64 (in LDS, any order), how many in s.npick
+    // logits put on a list (in any order), how many in s.npick
     if (t == 0) s.npick = 0;
-    auto put = [&](float z, int id) {
+    auto put = [&](int place) {
       const uint32_t at = atomicAdd(&s.npick, 1u);
-      if (at < (uint32_t)kWave) o.few[at] = make_uint2(__float_as_uint(z), (uint32_t)id);
+      if (at < (uint32_t)kFdOneList) o.few[at] = (uint16_t)place;
+    };
+    auto held = [&](int place) {
+      const uint32_t word = reinterpret_cast<const uint32_t*>(kept)[place * (int)sizeof(T) / 4];
+      return __uint_as_float(sizeof(T) == 4 ? word : place & 1 ? word & 0xffff0000u : word << 16);
+    };
+    auto listed = [&](int n, auto put) {             // those of a list
+      if (t < n) {
+        const float z = held(o.few[t]);
+        put(fd_key<T>(z), z);
+      }
     };
     bool done = false;
+    int nlist = kFdOneList + 1;                      // top-k's list, if it fits
     uint32_t low = kFdLowest<T>;
     if (by_k) {
       if (f.k <= kFdThreads) {
@@ -1290,22 +1306,22 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
             unpack(kept[q], v, T{});
 #pragma unroll
             for (int j = 0; j < N; ++j)
-              if (fd_key<T>(v[j]) >= low) put(v[j], row.first(q) + j);
+              if (fd_key<T>(v[j]) >= low) put(q * N + j);
           }
         __syncthreads();
-        const int n = (int)s.npick;
+        const int n = nlist = (int)s.npick;
         if (n <= kWave) {
           // all that matters in one wave's hands
           done = true;
           if (wave == 0) {
-            const uint2 e = o.few[lane];
-            const float z = lane < n ? __uint_as_float(e.x) : m;
+            const int place = lane < n ? o.few[lane] : 0;
+            const float z = lane < n ? held(place) : m;
             const double w = weight(z);
             const FdShort k1 = fd_short(fkey(z), lane < n ? fd_fixed(w, unit) : 0ull, n, true, f.k, by_p,
                                         (double)f.p, 0.0);
             const bool in = k1.kept && z >= tau;
             double S;
-            y = fd_short_draw(in, (int)e.y, w, n, a.tokens != nullptr, u, S);
+            y = fd_short_draw(in, place - row.off, w, n, a.tokens != nullptr, u, S);
             const uint32_t least = ~wave_max_u32(in ? ~fkey(z) : 0u);
             if (lane == 0) {
               o.tau = unkey(least);
@@ -1317,18 +1333,24 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
           invS = 1.0 / o.S;
         }
       }
-      if (!done)
-        low = fd_search<kFdThreads, false, false, T>(s, low, high, 0, (double)f.k, each,
-                                                  [](float) { return 0ull; }).low;
     }
-    if (by_p && by_k && !done) {
-      unsigned long long sum = 0, all;
-      each([&](uint32_t key, float z) {
-        if (key >= low) sum += fixed(z);
-      });
-      fd_block_scan<kFdWaves>(s, sum, all);
-      low = fd_search<kFdThreads, true, false, T>(s, low, high, 0, (double)f.p * (double)all, each,
-                                               fixed).low;
+    if (by_k && !done) {
+      // all that matters is on the list, or in the row
+      auto some = [&](auto put) {
+        if (nlist <= kFdOneList) listed(nlist, put);
+        else each(put);
+      };
+      low = fd_search<kFdThreads, false, false, T>(s, low, high, 0, (double)f.k, some,
+                                                [](float) { return 0ull; }).low;
+      if (by_p) {
+        unsigned long long sum = 0, all;
+        some([&](uint32_t key, float z) {
+          if (key >= low) sum += fixed(z);
+        });
+        fd_block_scan<kFdWaves>(s, sum, all);
+        low = fd_search<kFdThreads, true, false, T>(s, low, high, 0, (double)f.p * (double)all, some,
+                                                 fixed).low;
+      }
     } else if (by_p && !by_k) {
       const double width = 1e-6 - log((1.0 - (double)f.p) / a.V);
       const double per = kFdBins / width;
@@ -1367,14 +1389,14 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           const uint32_t key = fd_key<T>(v[j]);
-          if (key >= k0 && key <= k1 && in_bin(v[j])) put(v[j], 0);
+          if (key >= k0 && key <= k1 && in_bin(v[j])) put(q * N + j);
         }
       }
       __syncthreads();
       const int n = (int)s.npick;
       const unsigned long long above = s.above;
       if (n <= kWave) {                              // every wave for itself
-        const float z = lane < n ? __uint_as_float(o.few[lane].x) : m;
+        const float z = lane < n ? held(o.few[lane]) : m;
         const unsigned long long w = lane < n ? fixed(z) : 0ull;
         const int lo32 = (int)(uint32_t)w, hi32 = (int)(uint32_t)(w >> 32);
         const uint32_t key = fd_key<T>(z);
@@ -1389,9 +1411,11 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
         low = fd_search<kFdThreads, true, false, T>(
                   s, k0, k1, above, target,
                   [&](auto add) {
-                    each([&](uint32_t key, float z) {
-                      if (key >= k0 && key <= k1 && in_bin(z)) add(key, z);
-                    });
+                    if (n <= kFdOneList) listed(n, add);
+                    else
+                      each([&](uint32_t key, float z) {
+                        if (key >= k0 && key <= k1 && in_bin(z)) add(key, z);
+                      });
                   },
                   fixed).low;
       }
@@ -1526,9 +1550,6 @@ size_t filter_workspace_bytes(int B, int L, int V, bool bf16) {
   if (V <= kFdOneV) return 0;
   return fd_layout((size_t)B * L, V, fd_segs(V, bf16)).bytes;
 }
-
-// The most LDS that a kernel asks for (the rest: the votes of __syncthreads_or).
-constexpr int kFdLds = 159 * 1024;
 
 template <typename F>
 hipError_t fd_allow_lds(F* kernel) {
