@@ -895,9 +895,9 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
 
 // One wave a segment that reaches its row's bracket: as many waves as the chip
 // holds take them in turn from the plans' list, as rows differ in what they leave
-// (256 x 152064 float32, filters mixed: 73 us for the call, 77 with one wave for
-// every segment, most of which ended at once).  17 us there, 10 at 64 x 128256
-// bfloat16: two dependent loads, then the logits.
+// (256 x 152064 float32, filters mixed: 73 us for the call at the time, 77 with one
+// wave for every segment, most of which ended at once).  12 us there, 10 at 64 x
+// 128256 bfloat16: two dependent loads, then the logits.
 template <typename T>
 __global__ __launch_bounds__(kFdStatThreads) void filter_collect_kernel(FdArgs a) {
   constexpr int N = FdRow<T>::N, kWaves = kFdStatThreads / kWave;
@@ -1193,9 +1193,16 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_probs_kernel(FdArgs a, 
 // exponentials gives the total and the bin of the threshold; fd_search finds the
 // value in it.
 //
-// Bound by the float64 arithmetic of one CU: 32000 bfloat16 logits with top-p take 21
-// us, 10 of them that pass; 69 rows of 20001 without filters 14 us.  Rows spread
-// over workgroups, as longer ones are, need four launches that take 35 us.
+// For top-k, and in top-p's bin, what is left goes on a list of places in the row:
+// up to 64 are one wave's, up to 512 are searched in the row's stead (one of 16000
+// with all three filters 19.6 -> 15.8 us at 64 rows).
+//
+// Bound by one CU: 32000 bfloat16 logits with top-p take 20 to 30 us, 10 to 19 of
+// them that pass, as few or most tokens lie in the bins (their LDS atomics; bins by
+// whole steps of the exponential's table, with three float64 operations fewer a
+// token, changed nothing); with top-k 13, with min-p 9; 69 rows of 20001 without
+// filters 14.  Spread over workgroups, as longer rows are, a row of 33000 takes 20
+// to 30, 23 and 17.
 constexpr int kFdOneGroups = 144;                   // groups of 64 vectors
 constexpr int kFdOneV = 32768;
 constexpr int kFdOneList = 512;                     // one to a thread
