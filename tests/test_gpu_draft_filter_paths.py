@@ -146,3 +146,20 @@ def test_largest_vocabulary_of_float32():
     for k in (0, 40):
         probs, tok = both(z, u, T, k, p, 0.0)
         assert check(z, u, T, k, p, 0.0, probs, tok) <= 1
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n", [63, 64, 65, 300, 511, 512, 513, 900])
+def test_lists_of_every_length(n, dtype):
+    # n equal logits around the threshold, a few above them, the rest far below
+    u = torch.tensor([0.0, 0.4, 0.9999])
+    for V in (1200, 20001, 32768, 40000):
+        z = logits(3, V, n + V, F32, 1.0, 0) - 6.0
+        at = torch.randperm(V, generator=torch.Generator().manual_seed(n))[:n + 5]
+        z[:, at] = 4.0
+        z[:, at[:5]] = torch.tensor([5.0, 5.5, 6.0, 6.5, 7.0])
+        z = z.to(dtype)
+        for f in ((1.0, 50, 1.0, 0.0), (1.0, 50, 0.6, 0.0), (1.0, n + 5, 0.9, 0.0), (1.0, 0, 0.8, 0.0),
+                  (0.7, 3, 0.9, 0.0), (1.0, n + 4, 1.0, 0.5)):
+            probs, tok = both(z, u, *f)
+            assert check(z, u, *f, probs, tok) <= 1
