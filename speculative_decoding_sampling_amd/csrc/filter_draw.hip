@@ -58,18 +58,21 @@ enum FdKind : int { kFdError = 0, kFdGreedy = 1, kFdDraw = 2 };
 // What is left to do for a row after its plan.
 enum FdNeed : int { kFdDone = 0, kFdSums = 1, kFdTopK = 2, kFdTopP = 4 };
 
-// A row's plan, and what the kernel that writes the probabilities reads.
+// A row's plan, and what the kernel that writes the probabilities reads.  The row
+// kernel's waves read the plan each for itself, and its first may be done before the
+// others have: what it finds has fields of its own, which no wave of it reads.
 struct FdPlan {
   int kind;
   int need;
   int best;          // greedy: the token
-  float m, tau;      // largest logit; a token is kept iff its logit >= tau (before the row
-                     // kernel: by min-p alone)
+  float m, tau;      // largest logit; min-p keeps a token iff its logit >= tau
   float lo, hi;      // the bracket
   float bound;       // no token below it is kept by top-p
   uint32_t listed;   // logits collected for the row
-  uint32_t pad;
-  double invT, invS, Z;
+  float cut;         // found: a token is kept iff its logit >= cut
+  double invT;
+  double invS;       // found
+  double Z;
 };
 static_assert(sizeof(FdPlan) == 64, "FdPlan is 64 bytes");
 
@@ -783,7 +786,7 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
   top = fd_block_max<kWaves>(s, top);
   const bool ok = f.ok && top > kNegInfKey && top != 0xffffffffu && u >= 0.f && u < 1.f;
   const float m = ok ? unkey(top) : 0.f;
-  FdPlan plan = {kFdError, kFdDone, -1, m, -INFINITY, -INFINITY, INFINITY, -INFINITY, 0u, 0u, 0.0, 0.0, 0.0};
+  FdPlan plan = {kFdError, kFdDone, -1, m, -INFINITY, -INFINITY, INFINITY, -INFINITY, 0u, -INFINITY, 0.0, 0.0, 0.0};
   int y = -1;
   if (ok && f.T == 0.f) {
     // the first group that reaches the maximum, and in it the first token
@@ -997,7 +1000,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
       const int y = fd_short_draw(k.kept, (int)entry.y, w, (int)n, a.tokens != nullptr, u, S);
       const uint32_t low = ~wave_max_u32(k.kept ? ~fkey(z) : 0u);
       if (lane == 0) {
-        a.plans[r].tau = unkey(low);
+        a.plans[r].cut = unkey(low);
         a.plans[r].invS = 1.0 / S;
         if (a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
       }
@@ -1103,7 +1106,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
   double S;
   const int y = fd_draw(s, row, seg, a.nseg, a.tokens != nullptr, u, tau, weight, S);
   if (t == 0) {
-    a.plans[r].tau = tau;
+    a.plans[r].cut = tau;
     a.plans[r].invS = 1.0 / S;
     if (a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
   }
@@ -1145,7 +1148,7 @@ __device__ __forceinline__ void fd_put_all(O* out, int e, int V, const float (&w
   }
 }
 
-// The probabilities: one wave a segment, which reads the groups that reach tau.
+// The probabilities: one wave a segment, which reads the groups that reach the cut.
 // Memory: 320 x 128256 float32, filters mixed, 31 us for 164 MB of writes, 5.3 TB/s,
 // with the kept logits' reads beside them.
 template <typename T, typename O>
@@ -1160,7 +1163,7 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_probs_kernel(FdArgs a, 
   O* out = static_cast<O*>(a.probs) + (size_t)b * a.psb + (size_t)l * a.psl;
   const double c = p.invT * 1.4426950408889634, m = p.m;
   const bool draws = p.kind == kFdDraw;
-  const uint32_t bits = draws ? fd_reach(x, p.tau) : 0u;
+  const uint32_t bits = draws ? fd_reach(x, p.cut) : 0u;
   float v[kFdGroups][N];
   if (bits) fd_load(row, (uint32_t)g << 4 | bits, lane, v);
 #pragma unroll
@@ -1172,7 +1175,7 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_probs_kernel(FdArgs a, 
     if (bits >> j & 1u) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (v[j][i] >= p.tau) w[i] = fd_prob(v[j][i], m, c, (float)p.invS);
+        if (v[j][i] >= p.cut) w[i] = fd_prob(v[j][i], m, c, (float)p.invS);
     }
     if (p.kind == kFdGreedy) {
 #pragma unroll
