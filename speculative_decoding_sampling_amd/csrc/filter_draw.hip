@@ -159,8 +159,11 @@ __device__ __forceinline__ bool fd_wants_sums(const FdParams& f, int V) {
 
 // Weights exp((z - m) / T), at most 1: exp64.h's method and table.  The entries
 // have their index taken from the exponent's place, so that adding k there leaves
-// 2^(k / N) in one operation.  What would be below e^-700 stays there and counts as
-// nothing in a draw; -inf is told apart by whoever sums.
+// 2^(k / N) in one operation.  What would be below e^-700 stays there, -inf too.
+//
+// A weight of at most kFdNothing counts as nothing, in a segment's mass too: it has
+// one only where a token in it counts, however many others there are (at u = 0 a draw
+// ends in the first that has one).
 constexpr double kFdNothing = 1e-290;
 template <int BITS>                                  // of the 9 of the table's index
 __device__ __forceinline__ double fd_table_entry(int i) {
@@ -168,7 +171,7 @@ __device__ __forceinline__ double fd_table_entry(int i) {
   return __hiloint2double(__double2hiint(v) - (i << (20 - BITS)), __double2loint(v));
 }
 
-// The sum of the weights at or above tau, finite.  No branches: the weights'
+// The sum of the weights at or above tau that count.  No branches: the weights'
 // chains of dependent operations and table reads overlap.
 template <typename E, int N>
 __device__ __forceinline__ double fd_sum(const E& weight, const float (&v)[N], float tau) {
@@ -176,7 +179,7 @@ __device__ __forceinline__ double fd_sum(const E& weight, const float (&v)[N], f
 #pragma unroll
   for (int i = 0; i < N; ++i) w[i] = weight(v[i]);
 #pragma unroll
-  for (int i = 0; i < N; ++i) s += v[i] >= tau && v[i] > -INFINITY ? w[i] : 0.0;
+  for (int i = 0; i < N; ++i) s += v[i] >= tau && w[i] > kFdNothing ? w[i] : 0.0;
   return s;
 }
 
@@ -818,7 +821,7 @@ __global__ __launch_bounds__(kFdPlanThreads) void filter_plan_kernel(FdArgs a) {
       for (int g = t; g < a.nseg; g += kFdPlanThreads) {
         const float4 x = gmax[g];
         const float big = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
-        const double w = big > -INFINITY ? ssum[g] * weight(big) : 0.0;
+        const double top = weight(big), w = top > kFdNothing ? ssum[g] * top : 0.0;
         seg[g] = w;
         mine += w;
       }
@@ -1080,7 +1083,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
         for (uint32_t e = t % 16; e < p.y; e += 16) {
           const float z = list[p.x + e];
           const double x = weight(z);
-          w += z >= tau ? x : 0.0;
+          w += z >= tau && x > kFdNothing ? x : 0.0;
         }
         w += dpp_f64<0xb1>(w);
         w += dpp_f64<0x4e>(w);
