@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "abi_checks.h"
+#include "strided.h"
 
 namespace specv {
 bool fp4_quantize_fits(int rows, int D);
@@ -45,9 +46,11 @@ specv_status_t check_filter_sizes(int B, int L, int V, specv_dtype_t dtype) {
   return SPECV_OK;
 }
 
-// Rows of n elements at strides that the furthest element can be indexed by.
-bool far(int B, int64_t sb, int L, int64_t sl, int64_t n) {
-  return sb < 0 || sl < 0 || (double)B * sb + (double)L * sl + n > 1.0e18;
+// Whether rows of n elements, size bytes each, have a stride below 0 or reach further
+// than any memory: byte offsets within 2^60 are what the kernels and checks hold.
+bool far(int B, int64_t sb, int L, int64_t sl, int64_t n, size_t size) {
+  return sb < 0 || sl < 0 ||
+         ((double)(B - 1) * sb + (double)(L - 1) * sl + n) * size > (double)((int64_t)1 << 60);
 }
 
 // Whether the rows of an array lie over each other.
@@ -59,17 +62,6 @@ bool self_overlap(const Rows& r) {
     return !outer && !inner;
   }
   return (r.B > 1 && r.sb < r.n) || (r.nk > 1 && r.sk < r.n);
-}
-
-// Whether a row of one array lies over a row of the other.
-bool rows_overlap(const Rows& a, const Rows& b) {
-  if (!a.p || !b.p) return false;
-  const size_t last = (size_t)(a.B - 1) * a.sb + (size_t)(a.nk - 1) * a.sk;
-  if (!overlaps_rows(Span{a.p, last + a.n}, b)) return false;
-  for (int i = 0; i < a.B; ++i)
-    for (int k = 0; k < a.nk; ++k)
-      if (overlaps_rows(Span{static_cast<const char*>(a.p) + i * a.sb + k * a.sk, a.n}, b)) return true;
-  return false;
 }
 
 }  // namespace
@@ -160,27 +152,30 @@ specv_status_t specv_filter(const void* logits, int64_t stride_b, int64_t stride
       misaligned(probs, ps) || misaligned(f.temperature_array, 4) || misaligned(f.top_k_array, 4) ||
       misaligned(f.top_p_array, 4) || misaligned(f.min_p_array, 4))
     return SPECV_EINVAL;
-  if (far(B, stride_b, L, stride_l, V) || (out_tokens && (far(B, u_stride_b, L, u_stride_l, 1) ||
-                                                          far(B, token_stride_b, L, token_stride_l, 1))) ||
-      (probs && far(B, probs_stride_b, L, probs_stride_l, V)))
+  if (far(B, stride_b, L, stride_l, V, zs) ||
+      (out_tokens && (far(B, u_stride_b, L, u_stride_l, 1, 4) ||
+                      far(B, token_stride_b, L, token_stride_l, 1, 4))) ||
+      (probs && far(B, probs_stride_b, L, probs_stride_l, V, ps)))
     return SPECV_EINVAL;
-  const size_t need = filter_workspace_bytes(B, L, V, dtype == SPECV_BF16);
-  if (need > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
-    return SPECV_EWORKSPACE;
   const Rows z = {logits, stride_b * zs, stride_l * zs, B, L, V * zs};
   const Rows ur = {out_tokens ? u : nullptr, (size_t)u_stride_b * 4, (size_t)u_stride_l * 4, B, L, 4};
   const Rows t = {out_tokens, (size_t)token_stride_b * 4, (size_t)token_stride_l * 4, B, L, 4};
   const Rows p = {probs, probs_stride_b * ps, probs_stride_l * ps, B, L, V * ps};
-  const Span ws = {workspace, need};
-  const Span arrays[4] = {{f.temperature_array, (size_t)B * 4}, {f.top_k_array, (size_t)B * 4},
-                          {f.top_p_array, (size_t)B * 4}, {f.min_p_array, (size_t)B * 4}};
-  if (self_overlap(t) || self_overlap(p) || rows_overlap(t, p) || rows_overlap(t, z) ||
-      rows_overlap(t, ur) || rows_overlap(p, z) || rows_overlap(p, ur))
-    return SPECV_EINVAL;
-  for (const Rows* r : {&z, &ur, &t, &p})
-    if (overlaps_rows(ws, *r)) return SPECV_EINVAL;
-  for (const Span& s : arrays)
-    if (overlap(s, ws) || overlaps_rows(s, t) || overlaps_rows(s, p)) return SPECV_EINVAL;
+  auto array = [](const void* at, size_t n) { return Rows{at, 0, 0, 1, 1, n}; };
+  const Rows params[4] = {array(f.temperature_array, (size_t)B * 4), array(f.top_k_array, (size_t)B * 4),
+                          array(f.top_p_array, (size_t)B * 4), array(f.min_p_array, (size_t)B * 4)};
+  if (self_overlap(t) || self_overlap(p) || rows_overlap(t, p)) return SPECV_EINVAL;
+  for (const Rows* o : {&t, &p}) {
+    if (rows_overlap(*o, z) || rows_overlap(*o, ur)) return SPECV_EINVAL;
+    for (const Rows& r : params)
+      if (rows_overlap(*o, r)) return SPECV_EINVAL;
+  }
+  const size_t need = filter_workspace_bytes(B, L, V, dtype == SPECV_BF16);
+  if (need > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
+    return SPECV_EWORKSPACE;
+  const Rows ws = array(workspace, need);
+  for (const Rows* r : {&z, &ur, &t, &p, &params[0], &params[1], &params[2], &params[3]})
+    if (rows_overlap(ws, *r)) return SPECV_EINVAL;
   return status(launch_filter(logits, stride_b, stride_l, dtype == SPECV_BF16, B, L, V, f, u,
                               u_stride_b, u_stride_l, out_tokens, token_stride_b, token_stride_l,
                               probs, probs_stride_b, probs_stride_l, probs && probs_dtype == SPECV_BF16,
