@@ -53,17 +53,6 @@ bool far(int B, int64_t sb, int L, int64_t sl, int64_t n, size_t size) {
          ((double)(B - 1) * sb + (double)(L - 1) * sl + n) * size > (double)((int64_t)1 << 60);
 }
 
-// Whether the rows of an array lie over each other.
-bool self_overlap(const Rows& r) {
-  if (!r.p) return false;
-  if (r.B > 1 && r.nk > 1) {
-    const bool outer = r.sk >= r.n && r.sb >= (size_t)(r.nk - 1) * r.sk + r.n;
-    const bool inner = r.sb >= r.n && r.sk >= (size_t)(r.B - 1) * r.sb + r.n;
-    return !outer && !inner;
-  }
-  return (r.B > 1 && r.sb < r.n) || (r.nk > 1 && r.sk < r.n);
-}
-
 }  // namespace
 }  // namespace specv
 

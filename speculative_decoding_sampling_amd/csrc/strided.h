@@ -92,4 +92,16 @@ inline bool rows_overlap(const Rows& a, const Rows& b) {
   return false;
 }
 
+// Whether the rows of an array lie over each other: two of them, d apart along the
+// shorter axis and e along the other.
+inline bool self_overlap(const Rows& r) {
+  if (!r.p || r.n == 0) return false;
+  const Axes x = axes(r);
+  const int64_t near = (int64_t)r.n - 1;
+  if (x.many.n > 1 && x.many.s <= near) return true;                     // d = 0
+  for (int64_t d = 1; d < x.few.n; ++d)
+    if (any_in(d * x.few.s, x.many.s, 1 - x.many.n, x.many.n - 1, -near, near)) return true;
+  return false;
+}
+
 }  // namespace specv

@@ -22,6 +22,10 @@ extern "C" int overlap_of(const long long* a, const long long* b) {
   };
   return rows_overlap(rows(a), rows(b));
 }
+extern "C" int overlaps_itself(const long long* a) {
+  return self_overlap(Rows{reinterpret_cast<const void*>(a[0]), (size_t)a[1], (size_t)a[2], (int)a[3],
+                           (int)a[4], (size_t)a[5]});
+}
 """
 
 
@@ -129,3 +133,31 @@ def test_overlaps_come_before_a_missing_workspace(lib):  # noqa: F811
     # a stride that no row takes does not matter
     assert call_filter(lib, B=1, psb=1 << 62, zsb=1 << 62, ws=None) == EWORKSPACE
     assert call_filter(lib, psb=1 << 58, ws=None) == EINVAL
+
+
+def meets_itself(a):
+    r = sorted(rows(a))
+    return any(x[1] > y[0] for x, y in zip(r, r[1:]))
+
+
+def test_rows_of_one_array_against_every_pair(checks):
+    rng = random.Random(3)
+    seen = [0, 0]
+    for i in range(60000):
+        a = some(rng, rng.choice([5, 60, 400]))
+        want = meets_itself(a)
+        assert bool(checks.overlaps_itself(packed(a))) == want, a
+        seen[want] += 1
+    assert min(seen) > 10000
+
+
+def test_strides_that_are_not_nested_are_accepted(lib):  # noqa: F811
+    # rows at 0, 2, 4 and 3, 5, 7 times their length
+    V = 40000
+    kw = dict(B=3, L=2, V=V, zsb=2 * V, zsl=V, ws=None)
+    assert call_filter(lib, **kw, psb=2 * V, psl=3 * V, tsb=2, tsl=3) == EWORKSPACE
+    assert call_filter(lib, **kw, psb=3 * V, psl=2 * V, tsb=3, tsl=4) == EWORKSPACE
+    # at 0, 2, 4 and 4, 6, 8; one element short
+    assert call_filter(lib, **kw, psb=2 * V, psl=4 * V) == EINVAL
+    assert call_filter(lib, **kw, tsb=2, tsl=4) == EINVAL
+    assert call_filter(lib, **kw, psb=2 * V, psl=3 * V - 1) == EINVAL
