@@ -16,7 +16,7 @@
 // multiples of 2^-s, s = 62 - ceil(log2 V) but at most 51: integer sums do not
 // depend on their order, so that the histograms may be built with atomics, and n
 // tokens are off by at most n 2^-(s+1) of the largest weight.  The sums of a draw are
-// float64 in a fixed order.
+// float64 in a fixed order.  Probabilities are float64 up to their rounding.
 //
 // Split.  A row is cut into groups, one 16-byte vector for each lane of a wave,
 // and segments of four groups.
@@ -1115,14 +1115,6 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
   }
 }
 
-// 2^x / S for x = (z - m) / (T ln 2): the argument in float64, its fraction's
-// power by the hardware's exp2 (1 ulp).
-__device__ __forceinline__ float fd_prob(float z, double m, double c, float invS) {
-  const double x = fmax(((double)z - m) * c, -1000.0);
-  const double k = rint(x);
-  return ldexpf(__builtin_amdgcn_exp2f((float)(x - k)) * invS, (int)k);
-}
-
 __device__ __forceinline__ void fd_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void fd_put(bf16_t* p, float v) { *p = bf16_bits(v); }
 
@@ -1164,7 +1156,7 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_probs_kernel(FdArgs a, 
   const FdPlan p = a.plans[r];
   const float4 x = a.gmax[(size_t)r * a.nseg + g];
   O* out = static_cast<O*>(a.probs) + (size_t)b * a.psb + (size_t)l * a.psl;
-  const double c = p.invT * 1.4426950408889634, m = p.m;
+  const FdWaveExp weight(p.m, p.invT);
   const bool draws = p.kind == kFdDraw;
   const uint32_t bits = draws ? fd_reach(x, p.cut) : 0u;
   float v[kFdGroups][N];
@@ -1175,10 +1167,12 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_probs_kernel(FdArgs a, 
     float w[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i] = 0.f;
-    if (bits >> j & 1u) {
+    if (bits >> j & 1u) {                            // (all lanes: the table is spread over them)
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (v[j][i] >= p.cut) w[i] = fd_prob(v[j][i], m, c, (float)p.invS);
+      for (int i = 0; i < N; ++i) {
+        const float x = (float)(weight(v[j][i]) * p.invS);
+        w[i] = v[j][i] >= p.cut ? x : 0.f;
+      }
     }
     if (p.kind == kFdGreedy) {
 #pragma unroll
@@ -1510,7 +1504,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
   if (t == 0 && a.tokens) a.tokens[(size_t)b * a.tsb + (size_t)l * a.tsl] = y;
   if (a.probs) {
     O* out = static_cast<O*>(a.probs) + (size_t)b * a.psb + (size_t)l * a.psl;
-    const double c = invT * 1.4426950408889634;
+    const FdExp weight(m, invT, s.tbl);
     for (int q = t; q < nv; q += kFdThreads) {
       const int e = row.first(q);
       float v[N], w[N];
@@ -1518,7 +1512,7 @@ __global__ __launch_bounds__(kFdThreads) void filter_one_kernel(FdArgs a) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         w[j] = 0.f;
-        if (ok && v[j] >= tau) w[j] = fd_prob(v[j], m, c, (float)invS);
+        if (ok && v[j] >= tau) w[j] = (float)(weight(v[j]) * invS);
         if (ok && f.T == 0.f) w[j] = e + j == y ? 1.f : 0.f;
       }
       fd_put_all(out, e, a.V, w);
