@@ -1032,13 +1032,14 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
   if (by_k || by_p) {
     FdSource<T> src = {row, picks, 0u, list, n, true};
     auto each = [&](auto put) { src.each([&](float z) { put(fd_key<T>(z), z); }); };
+    const double share = (double)f.p * plan.Z * unit;    // top-p's, where top-k is off
     auto search = [&](float from, uint32_t top, unsigned long long above) -> FdFound {
       FdFound k = {from > -INFINITY ? fd_key<T>(from) : kFdLowest<T>, true};
       if (by_k)
         k = fd_search<kFdThreads, false, false, T>(s, k.low, top, 0, (double)f.k, each,
                                                 [](float) { return 0ull; });
       if (by_p) {
-        double target = (double)f.p * plan.Z * unit;
+        double target = share;
         if (by_k) {
           unsigned long long sum = 0, all;
           each([&](uint32_t key, float z) {
@@ -1053,11 +1054,12 @@ __global__ __launch_bounds__(kFdThreads) void filter_row_kernel(FdArgs a) {
       return k;
     };
     FdFound k = {0u, false};
-    if (whole && (by_k || high < (double)f.p * plan.Z)) {
+    const unsigned long long above = (unsigned long long)__double2ll_rn(high * unit);
+    if (whole && (by_k || (double)above < share)) {
       // (the range that the list covers, so that its bins are fine)
-      k = search(plan.lo, fd_key<T>(fminf(plan.hi, m)), (unsigned long long)__double2ll_rn(high * unit));
-      // not reached: the threshold lies below the bracket, and below min-p's if
-      // the bracket starts there
+      k = search(plan.lo, fd_key<T>(fminf(plan.hi, m)), above);
+      // not reached, with less than the share above: the threshold lies below the
+      // bracket, and below min-p's if the bracket starts there
       if (!k.reached && plan.lo == plan.tau)
         k = {plan.lo > -INFINITY ? fd_key<T>(plan.lo) : kFdLowest<T>, true};
     }
