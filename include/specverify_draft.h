@@ -139,9 +139,11 @@ typedef struct {
  *   p(v) = exp((z(v) - max z) / T) / S over the kept tokens, 0 elsewhere,
  * S their sum, and its token the first id whose running sum of the kept
  * weights exceeds u S (ids ascending, strict comparison, as specv_sample
- * draws; a weight below 1e-290 of the largest counts as nothing).  The kept set
- * is decided on weights held to 2^-62 V of the largest (at least 2^-51), the
- * draw sums in float64; results do not change from run to run.
+ * draws; a weight of at most 1e-290 of the largest counts as nothing).  Weights
+ * are float64, good to 1e-13 of their size down to 100 T below the largest logit.
+ * Min-p is decided on a weight, top-p on sums of weights in whole multiples of
+ * 2^-s of the largest one, s = 62 - ceil(log2 V) but at most 51; the draw sums in
+ * float64.  Results do not change from run to run.
  *
  *  logits      row l of request b starts at element b * stride_b + l *
  *              stride_l, V consecutive values of dtype, any alignment of an

@@ -12,7 +12,9 @@
 // less than p of the mass: both are a search, from the top, for the value at
 // which a running count or mass reaches a target.
 //
-// Numerics.  Weights are float64.  A mass that decides tau_p is a sum of whole
+// Numerics.  Weights are float64, good to 1e-13 of their size up to 100 T below the
+// maximum (4e-14 the coarser of the two exponentials, the rest the argument's
+// roundings).  A mass that decides tau_p is a sum of whole
 // multiples of 2^-s, s = 62 - ceil(log2 V) but at most 51: integer sums do not
 // depend on their order, so that the histograms may be built with atomics, and n
 // tokens are off by at most n 2^-(s+1) of the largest weight.  The sums of a draw are
@@ -1147,7 +1149,9 @@ __device__ __forceinline__ void fd_put_all(O* out, int e, int V, const float (&w
 
 // The probabilities: one wave a segment, which reads the groups that reach the cut.
 // Memory: 320 x 128256 float32, filters mixed, 31 us for 164 MB of writes, 5.3 TB/s,
-// with the kept logits' reads beside them.
+// with the kept logits' reads beside them.  (Probabilities by the hardware's float32
+// exp2 take a microsecond less, 3 where nothing is filtered, and are off by up to 2.7
+// half steps.)
 template <typename T, typename O>
 __global__ __launch_bounds__(kFdStatThreads) void filter_probs_kernel(FdArgs a, int nblk) {
   constexpr int N = FdRow<T>::N;
@@ -1203,7 +1207,7 @@ __global__ __launch_bounds__(kFdStatThreads) void filter_probs_kernel(FdArgs a, 
 // them that pass, as few or most tokens lie in the bins (their LDS atomics; bins by
 // whole steps of the exponential's table, with three float64 operations fewer a
 // token, changed nothing); with top-k 13, with min-p 9; 69 rows of 20001 without
-// filters 14.  Spread over workgroups, as longer rows are, a row of 33000 takes 20
+// filters 15.  Spread over workgroups, as longer rows are, a row of 33000 takes 20
 // to 30, 23 and 17.
 constexpr int kFdOneGroups = 144;                   // groups of 64 vectors
 constexpr int kFdOneV = 32768;

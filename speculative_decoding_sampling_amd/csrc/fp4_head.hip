@@ -254,14 +254,19 @@ __global__ __launch_bounds__(kF4Threads) void fp4_skinny_kernel(
 // them, each fragment feeding two products.  A run is two steps of 8-bit or
 // four of 4-bit states.
 //
-// 1152 x 152064 x 4096 takes 590 us with 8-bit states, 2.4 PFLOP/s: the matrix cores
-// are busy 65 % of the cycles, at 1.73 GHz, the power limit (a loop of nothing but
-// such products does 4.0 on zeros and ones); with 4-bit states 450 to 470 us, 3.1
-// PFLOP/s, busy 39 % at 2.03 GHz.  Those wait for operands: without its weight loads
-// the kernel takes 388, without those of the hidden rows 442.  Weights three runs
-// ahead instead of one (96 rows, which have the registers) took 536 us against 517;
-// a wave's priority raised over its products changed nothing, steps kept apart cost
-// 3 %.
+// Bound by operands on their way to the products and by the stores.  1152 x 152064 x
+// 4096 takes 590 us with 8-bit states, 2.4 PFLOP/s, the matrix cores busy 65 % of
+// the cycles at 1.8 GHz: without its weight loads 505, without those of the hidden
+// rows 527, without either 455, without the stores of the logits 543.  With 4-bit
+// states 451 us, 3.2 PFLOP/s, busy 39 % at 2.0 GHz, and 352, 409, 317 and 388; at 320
+// x 128256 132 us, and 90, 121, 81 and 115.  (A loop of nothing but such products does
+// 4.0 and 7.3 PFLOP/s, on zeros and ones.)  Float32 logits: of 8-bit states 1130 us,
+// and 305 at 320 x 128256, a large library product's rate in bfloat16, the type that
+// they take; of 4-bit states 522 and 150.
+//
+// Weights three runs ahead instead of one (96 rows, which have the registers) took 536
+// us against 517; a wave's priority raised over its products changed nothing, steps
+// kept apart cost 3 %.
 //
 // Rows of a staged run have their eight 16-byte pieces swapped by row pair (row
 // r's piece p at slot p ^ ((r >> 1) & 7)), so that 16 consecutive rows cover
